@@ -466,6 +466,147 @@ int w4a16_gemm_split_packed(const float *X, const void *packed, float *Y, int64_
                             void *stream);
 
 /*
+ * Mixture-of-experts layer around the grouped GEMM: routing of tokens to
+ * experts, the experts' gate/up projections with their SwiGLU epilogue, and
+ * their down projections combined back into the tokens.  The activations are
+ * fp32, fp16 or bf16 (W4A16_DTYPE_*); sums are fp32, and each 16-bit output is
+ * rounded once.  A caller runs
+ *     w4a16_moe_route            logits -> ids, weights, slots, token_index,
+ *                                          expert_offsets
+ *     w4a16_gemm_grouped_swiglu  X -> H, one row per slot
+ *     w4a16_gemm_grouped_combine H -> Y, one row per token
+ * The lists are those of w4a16_gemm_grouped as well.  All pointers are DEVICE
+ * memory.  Nothing is allocated and no call waits for the GPU, so a layer can
+ * be captured into a HIP graph; two calls that share a workspace must not run
+ * at the same time.  Results do not depend on timing (no floating-point
+ * atomics).
+ */
+#define W4A16_DTYPE_F32 0
+#define W4A16_DTYPE_F16 1
+#define W4A16_DTYPE_BF16 2
+
+#define W4A16_SCORE_SOFTMAX 0
+#define W4A16_SCORE_SIGMOID 1
+
+#define W4A16_ROUTE_MAX_EXPERTS 1024
+#define W4A16_ROUTE_MAX_TOPK 32
+#define W4A16_ROUTE_MAX_GROUPS 64
+
+/* Workspace bytes of w4a16_moe_route (0 up to 64 tokens, or for extents it
+ * refuses).  Host only. */
+size_t w4a16_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t topk);
+
+/*
+ * Route T tokens to topk of E experts each and build the slot lists.
+ *   logits          [T][E], dtype     router outputs
+ *   bias            float [E]         added to the scores for the choice only; may be NULL
+ *   num_tokens      int32 [1]         tokens in use, clamped to [0, T]; NULL: all T
+ *   ids             int32 [T][topk]   experts of a token, best first; -1: no expert
+ *   weights         float [T][topk]   their weights; 0 where ids is -1
+ *   slots           int32 [T][topk]   their slots; -1 where ids is -1
+ *   token_index     int32 [T*topk]    token of each slot; -1 behind the last one
+ *   expert_offsets  int32 [E+1]       expert e owns slots [offsets[e], offsets[e+1])
+ * Per token: score s_e = 1 / (1 + exp(-l_e)), or the softmax over the token's
+ * logits; key c_e = s_e + bias_e.  With group_limit < groups, experts are
+ * taken from group_limit of `groups` runs of E / groups neighbouring experts
+ * only: a group is worth the sum of its group_top (1 or 2) largest keys, and
+ * the largest groups stay.  The topk largest keys are chosen.  Ties go to the
+ * lower index.  weights = s of the chosen (divided by their sum if
+ * renormalize is not 0; 0 if that sum is 0) times scale.  Slots are sorted by
+ * expert, then token.
+ * The choice is that of keys computed in 64 bits (without a bias, of the
+ * logits, whose order the scores have).  An expert whose logit is NaN or -inf,
+ * or whose bias makes its key so, is masked: it adds nothing to its group and
+ * is never chosen; a token with fewer than topk experts left ends with -1.
+ * Tokens from num_tokens on get -1 throughout and no slot.
+ * T == 0 writes expert_offsets alone.  W4A16_ERR_ARG for a NULL required
+ * pointer, topk > E, groups that do not divide E, group_limit outside
+ * [1, groups], an unknown score, dtype or group_top, a scale that is not
+ * finite, an output that overlaps an input or another output, or a missing,
+ * misaligned (256 bytes), too small or overlapping workspace;
+ * W4A16_ERR_SHAPE for E, topk or groups above W4A16_ROUTE_MAX_* or
+ * T * topk >= 2^31; W4A16_ERR_ALIGN for pointers not aligned to their elements.
+ */
+int w4a16_moe_route(const void *logits, const float *bias, const int32_t *num_tokens,
+                    int32_t *ids, float *weights, int32_t *slots, int32_t *token_index,
+                    int32_t *expert_offsets, int64_t T, int64_t E, int64_t topk, int32_t score,
+                    int64_t groups, int64_t group_limit, int32_t group_top, int32_t renormalize,
+                    float scale, int32_t dtype, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/* Kernels behind w4a16_gemm_grouped_swiglu and w4a16_gemm_grouped_combine. */
+#define W4A16_EXPERTS_SKINNY 1 /* few slots per expert: weights and activations from memory to
+                                  registers, K split over the 8 waves of a workgroup */
+#define W4A16_EXPERTS_TILE 2   /* many: 128 x 128 tiles on fp16 limbs of the activations
+                                  (made in the workspace) */
+
+/* The kernel for R slots over E experts (one of W4A16_EXPERTS_*), 0 for
+ * extents that are refused or a no-op.  Host only. */
+int w4a16_experts_kernel(int64_t R, int64_t E);
+
+/* Workspace bytes of w4a16_gemm_grouped_swiglu (0 for the skinny kernel and
+ * for extents it refuses).  Host only. */
+size_t w4a16_grouped_swiglu_workspace_bytes(int64_t T, int64_t R, int64_t E, int64_t F, int64_t K,
+                                            int32_t dtype);
+
+/*
+ * The experts' fused gate/up projection: for slot r of expert e, x =
+ * X[token_index[r]],
+ *     H[r][j] = silu(x . gate_j) * (x . up_j),
+ * gate_j and up_j rows j and F + j of expert e's weights.
+ *   X               [T][K], dtype       tokens
+ *   token_index     int32 [R]
+ *   expert_offsets  int32 [E+1]         as w4a16_gemm_grouped; offsets[E] may be below R:
+ *                                       rows of H from offsets[E] on are left as they were
+ *   qweight         int32 [E][2F][K/8], scales float [E][2F][K/32]
+ *   H               [R][F], dtype
+ * The weights of an expert without slots are not read.  token_index and
+ * expert_offsets are clamped into range on the device.  fp32 activations meet
+ * the tolerance of w4a16_gemm on both sums, and so do fp16 ones.  bf16 ones
+ * meet it with scale * |x| * (q + 40) in place of |x * w| (the skinny kernel
+ * multiplies by q + 16 and takes 24 off again in fp32); the tile kernel scales
+ * them per row into fp16, exactly for values down to 2^-28 of their row's
+ * largest.  A row of X holding Inf or NaN gives non-finite values in its slots.
+ * workspace: w4a16_grouped_swiglu_workspace_bytes, 256-byte aligned; may be
+ * NULL where that is 0.  R == 0 or F == 0 is a no-op; T == 0 with R > 0 is
+ * W4A16_ERR_ARG; an unknown dtype is W4A16_ERR_ARG; X and qweight 16-byte
+ * aligned, H to its elements; otherwise errors as w4a16_gemm_grouped with
+ * N = 2F.
+ */
+int w4a16_gemm_grouped_swiglu(const void *X, const int32_t *token_index,
+                              const int32_t *expert_offsets, const int32_t *qweight,
+                              const float *scales, void *H, int64_t T, int64_t R, int64_t E,
+                              int64_t F, int64_t K, int32_t group, int32_t dtype, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of w4a16_gemm_grouped_combine (0 for extents it refuses or
+ * a no-op).  Host only. */
+size_t w4a16_grouped_combine_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t N,
+                                             int64_t K, int32_t dtype);
+
+/*
+ * The experts' down projections, combined:
+ *     Y[t][n] = sum_j weights[t][j] * (H[slots[t][j]] . W_e[n]),
+ * e the expert that owns the slot.
+ *   H               [T*topk][K], dtype     one row per slot
+ *   expert_offsets  int32 [E+1]
+ *   qweight         int32 [E][N][K/8], scales float [E][N][K/32]
+ *   slots           int32 [T][topk]        below 0: no term (its weight is not used)
+ *   weights         float [T][topk]
+ *   Y               [T][N], dtype          0 for a token without a slot
+ * The slots' products are kept in fp32 (in the workspace) and added in the
+ * order of j.  Rows of H from expert_offsets[E] on are never used; a slot that
+ * no expert owns gives an undefined row.  Slots past T*topk - 1 are clamped.
+ * workspace: w4a16_grouped_combine_workspace_bytes, 256-byte aligned.
+ * T == 0 or N == 0 is a no-op.  Otherwise as w4a16_gemm_grouped_swiglu.
+ */
+int w4a16_gemm_grouped_combine(const void *H, const int32_t *expert_offsets,
+                               const int32_t *qweight, const float *scales, const int32_t *slots,
+                               const float *weights, void *Y, int64_t T, int64_t topk, int64_t E,
+                               int64_t N, int64_t K, int32_t group, int32_t dtype,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Raw weight files of one quantized weight W[N][K], as the pages' INT4 model
  * bundles store them: "<name>.qw" holds qweight[N][K/8] as little-endian int32
  * and "<name>.sc" holds scales[N][K/32] as little-endian fp32, both row-major

@@ -133,4 +133,46 @@ hipError_t launch_read_floor(const void *const *ptrs, const long *bytes, int n, 
                              int loads, unsigned *sink, hipStream_t stream);
 
 
+// ---- mixture of experts: routing, experts' products, combination of slots
+
+// One routing call (moe_route.hip); validated by the C-ABI layer.
+struct MoeRoute {
+  const void *logits;         // [T][E], dtype
+  const float *bias;          // [E] or NULL
+  const int32_t *num_tokens;  // device word or NULL
+  int32_t *ids;
+  float *weights;
+  int32_t *slots, *token_index, *expert_offsets;
+  int T, E, topk, groups, group_limit, group_top, sigmoid, renormalize, dtype;
+  float scale;
+};
+size_t route_workspace_bytes(long T, int E);
+hipError_t launch_route(const MoeRoute &r, void *workspace, hipStream_t stream);
+
+// The experts' products over routed slots: with `swiglu`, W has 2N rows and
+// Y[R][ldy] = silu(gate) * up in the activations' type; else Y is fp32.
+struct MoeExperts {
+  const void *X;                // [rows_x][K], dtype
+  const int32_t *token_index;   // [R]: row of X of a slot; NULL: the slot itself
+  const int32_t *expert_offsets;
+  const int32_t *qweight;
+  const float *scales;
+  void *Y;
+  void *workspace;              // experts_workspace_bytes bytes
+  int rows_x, R, E, N, K, ldy, dtype;
+  bool swiglu;
+};
+// W4A16_EXPERTS_*: the kernel for a shape; its workspace (0 for the skinny one)
+int experts_kernel(long R, long E);
+size_t experts_workspace_bytes(long rows_x, long R, long E, int K, int dtype);
+hipError_t launch_experts(const MoeExperts &p, hipStream_t stream);
+int experts_skinny_rows(long R, long E);
+hipError_t launch_experts_skinny(const MoeExperts &p, hipStream_t stream);
+hipError_t launch_experts_tile(const MoeExperts &p, hipStream_t stream);
+
+// Y[t][n] = sum_j weights[t][j] * D[slots[t][j]][n], D fp32 [R][ldd], Y [T][N]
+// in dtype; slots below 0 add nothing.
+hipError_t launch_combine(const float *D, const int32_t *slots, const float *weights, void *Y,
+                          int T, int topk, int R, int N, int ldd, int dtype, hipStream_t stream);
+
 }  // namespace w4a16

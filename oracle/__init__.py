@@ -38,3 +38,9 @@ from .w4a16_ref import (  # noqa: F401
     SLAB,
     STAGE_GROUPS,
 )
+from .moe_ref import (  # noqa: F401,E402
+    experts_combine,
+    experts_swiglu,
+    route,
+    slot_lists,
+)

@@ -1,0 +1,298 @@
+"""GPU parity of the experts' products (w4a16_gemm_grouped_swiglu,
+w4a16_gemm_grouped_combine) and of the whole layer with its routing."""
+
+import sys
+
+import numpy as np
+import pytest
+
+import oracle
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import int4_weight_only_03_amd as pkg  # noqa: E402
+
+TYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+
+
+def say(*a):
+    print(*a, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm device")
+    pkg.load()
+    return torch.device("cuda:0")
+
+
+def weights_of(rng, E, rows, K):
+    """Random nibbles and group scales of both signs' worth of magnitude."""
+    qw = rng.integers(-(2 ** 31), 2 ** 31, (E, rows, K // 8), dtype=np.int64).astype(np.int32)
+    sc = (0.003 + 0.002 * rng.random((E, rows, K // 32))).astype(np.float32)
+    return qw, sc
+
+
+def activations(rng, rows, K, dtype):
+    """(device tensor of the type, its values in fp32), rows of different sizes"""
+    x = rng.standard_normal((rows, K)) * 2.0 ** rng.integers(-3, 4, (rows, 1))
+    t = torch.from_numpy(x.astype(np.float32)).to(TYPES[dtype])
+    return t.to("cuda:0"), t.float().numpy()
+
+
+def lists_of(counts, T, rng):
+    """Slot lists with counts[e] slots of expert e, tokens at random."""
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    return rng.integers(0, T, off[-1]).astype(np.int32), off
+
+
+def on(dev, *arrays):
+    return [torch.from_numpy(np.ascontiguousarray(a)).to(dev) for a in arrays]
+
+
+def within(got, want, tol, what):
+    got = got.float().cpu().numpy().astype(np.float64)
+    assert np.all(np.isfinite(got))
+    err = np.abs(got - want)
+    say(f"  {what}: max err/bound {np.max(err / tol) if err.size else 0:.3e}")
+    assert np.all(err <= tol)
+
+
+def run_swiglu(dev, counts, T, F, K, dtype, seed, spare=0):
+    """`spare`: rows of H behind the last slot, which stay as they were"""
+    rng = np.random.default_rng(seed)
+    E = len(counts)
+    tok, off = lists_of(counts, T, rng)
+    qw, sc = weights_of(rng, E, 2 * F, K)
+    Xd, X = activations(rng, T, K, dtype)
+    R = len(tok) + spare
+    tokd = torch.full((R,), -1, dtype=torch.int32, device=dev)
+    tokd[:len(tok)] = torch.from_numpy(tok).to(dev)
+    offd, qwd, scd = on(dev, off, qw, sc)
+    pad = 1024
+    buf = torch.full((pad + R * F + pad,), 77.0, dtype=TYPES[dtype], device=dev)
+    Hd = buf[pad:pad + R * F].view(R, F)
+    out = pkg.w4a16_gemm_grouped_swiglu(Xd, tokd, offd, qwd, scd, Hd)
+    torch.cuda.synchronize()
+    assert out is Hd
+    assert torch.all(buf[:pad] == 77) and torch.all(buf[pad + len(tok) * F:] == 77)
+    H, tol = oracle.experts_swiglu(X, tok, off, qw, sc, dtype)
+    within(Hd[:len(tok)], H, tol, f"swiglu {dtype}")
+    again = pkg.w4a16_gemm_grouped_swiglu(Xd, tokd, offd, qwd, scd)
+    assert torch.equal(again[:len(tok)], Hd[:len(tok)])
+
+
+SWIGLU = [
+    # counts, T, F, K, spare
+    ([1], 1, 1, 32, 0), ([0, 2, 0], 1, 33, 96, 0), ([1, 0, 0, 1], 1, 16, 128, 3),
+    ([3, 1, 16, 17], 9, 70, 160, 0), ([15, 0, 33], 40, 45, 224, 5), ([8] * 8, 16, 64, 1056, 0),
+    ([1] * 70, 5, 17, 64, 1), ([0] * 130 + [2] + [0] * 69, 3, 20, 256, 0),
+    # blocks of 32 and 64 slots, with rest blocks
+    ([20, 33, 2], 25, 40, 288, 2), ([40, 64, 65, 1], 50, 50, 352, 0), ([63, 50], 99, 31, 96, 0),
+    # the tile kernel: odd sizes, an odd number of groups, empty experts, rest tiles
+    ([64, 0], 30, 64, 64, 64), ([128, 129, 1], 200, 65, 96, 0), ([300, 0, 5, 90], 111, 130, 160, 7),
+    ([512], 77, 1, 32, 0), ([200, 190], 400, 200, 544, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("counts,T,F,K,spare", SWIGLU)
+def test_swiglu_shapes(dev, counts, T, F, K, spare, dtype):
+    E, R = len(counts), sum(counts) + spare
+    say("swiglu", counts[:8], T, F, K, dtype, "kernel", pkg.w4a16_experts_kernel(R, E))
+    run_swiglu(dev, counts, T, F, K, dtype, seed=R + F + K, spare=spare)
+
+
+def test_swiglu_decode_batch(dev):
+    # 16 tokens, top-4 of 32 experts, 512 gate and up rows of 7168 features
+    counts = np.bincount(np.random.default_rng(3).integers(0, 32, 64), minlength=32)
+    for dtype in TYPES:
+        run_swiglu(dev, counts, 16, 512, 7168, dtype, seed=4)
+
+
+def combine_case(dev, rng, T, topk, E, N, K, dtype, live=None, H=None):
+    """Distinct experts per token; tokens from `live` on have none."""
+    ids = np.stack([rng.permutation(E)[:topk] for _ in range(T)]).astype(np.int32)
+    ids[T if live is None else live:] = -1
+    slots, tok, off = oracle.slot_lists(ids, E)
+    w = rng.standard_normal((T, topk)).astype(np.float32)
+    qw, sc = weights_of(rng, E, N, K)
+    Hd, Hv = activations(rng, T * topk, K, dtype) if H is None else H
+    return Hd, Hv, off, qw, sc, slots, w
+
+
+COMBINE = [
+    # T, topk, E, N, K, live
+    (1, 1, 1, 1, 32, None), (1, 8, 8, 70, 96, None), (3, 2, 5, 33, 64, None),
+    (16, 4, 32, 130, 224, 13), (5, 3, 4, 1027, 160, 0), (61, 4, 12, 96, 352, None),
+    (100, 2, 6, 81, 256, 77), (130, 1, 3, 50, 32, None),
+    # the tile kernel
+    (128, 2, 4, 129, 96, None), (300, 2, 3, 64, 160, 290), (700, 1, 2, 200, 544, None),
+]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,topk,E,N,K,live", COMBINE)
+def test_combine_shapes(dev, T, topk, E, N, K, live, dtype):
+    say("combine", T, topk, E, N, K, live, dtype, "kernel", pkg.w4a16_experts_kernel(T * topk, E))
+    rng = np.random.default_rng(T + N + K)
+    Hd, Hv, off, qw, sc, slots, w = combine_case(dev, rng, T, topk, E, N, K, dtype, live)
+    Hd[off[-1]:] = float("nan")  # rows of no expert are not used
+    args = on(dev, off, qw, sc, slots, w)
+    pad = 1024
+    buf = torch.full((pad + T * N + pad,), 77.0, dtype=TYPES[dtype], device=dev)
+    Yd = pkg.w4a16_gemm_grouped_combine(Hd, *args, Y=buf[pad:pad + T * N].view(T, N))
+    torch.cuda.synchronize()
+    assert torch.all(buf[:pad] == 77) and torch.all(buf[pad + T * N:] == 77)
+    Y, tol = oracle.experts_combine(Hv, off, qw, sc, slots, w, dtype)
+    within(Yd, Y, tol, f"combine {dtype}")
+    assert torch.equal(pkg.w4a16_gemm_grouped_combine(Hd, *args), Yd)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T", [1, 20, 200])
+def test_layer(dev, T, dtype):
+    """Routing, experts and combination as one layer runs them, eager and captured;
+    the padded batch's last tokens come back as zeros."""
+    E, topk, F, K, N = 6, 3, 48, 96, 40
+    live = max(1, T - 3)
+    rng = np.random.default_rng(T)
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    gq, gs = weights_of(rng, E, 2 * F, K)
+    dq, ds = weights_of(rng, E, N, F // 32 * 32 + 32)
+    F = F // 32 * 32 + 32
+    gq, gs = weights_of(rng, E, 2 * F, K)
+    Xd, X = activations(rng, T, K, dtype)
+    ld, bd, gqd, gsd, dqd, dsd = on(dev, logits, bias, gq, gs, dq, ds)
+    n = torch.tensor([live], dtype=torch.int32, device=dev)
+
+    def layer():
+        r = pkg.w4a16_moe_route(ld, topk, bias=bd, score="sigmoid", groups=3, group_limit=2,
+                                num_tokens=n)
+        H = pkg.w4a16_gemm_grouped_swiglu(Xd, r.token_index, r.expert_offsets, gqd, gsd)
+        Y = pkg.w4a16_gemm_grouped_combine(H, r.expert_offsets, dqd, dsd, r.slots, r.weights)
+        return r, H, Y
+
+    def check(r, H, Y):
+        torch.cuda.synchronize()
+        x, lg = Xd.float().cpu().numpy(), ld.cpu().numpy()
+        ids, w = oracle.route(lg, topk, bias=bias, score="sigmoid", groups=3, group_limit=2,
+                              num_tokens=live)
+        slots, tok, off = oracle.slot_lists(ids, E)
+        assert np.array_equal(r.slots.cpu().numpy(), slots)
+        m = off[-1]
+        want, tol = oracle.experts_swiglu(x, tok[:m], off, gq, gs, dtype)
+        within(H[:m], want, tol, "layer H")
+        Hv = np.zeros((T * topk, F), np.float32)
+        Hv[:m] = H[:m].float().cpu().numpy()
+        want, tol = oracle.experts_combine(Hv, off, dq, ds, slots, r.weights.cpu().numpy(), dtype)
+        within(Y, want, tol, "layer Y")
+        assert torch.all(Y[live:] == 0)
+
+    check(*layer())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kept = layer()
+    for i in range(3):
+        Xd.copy_(activations(rng, T, K, dtype)[0])
+        ld.copy_(torch.randn(T, E, device=dev))
+        layer()
+        g.replay()
+        check(*kept)
+
+
+def test_lists_of_the_router_serve_the_grouped_gemm(dev):
+    """The plain grouped product takes the same lists."""
+    T, E, topk, N, K = 20, 5, 2, 40, 96
+    rng = np.random.default_rng(2)
+    Xd, X = activations(rng, T, K, "fp32")
+    qw, sc = weights_of(rng, E, N, K)
+    qwd, scd = on(dev, qw, sc)
+    r = pkg.w4a16_moe_route(torch.randn(T, E, device=dev), topk)
+    Y = pkg.w4a16_gemm_grouped(Xd, r.token_index, r.expert_offsets, qwd, scd)
+    v = oracle.compare_grouped(Y.cpu().numpy(), X, r.token_index.cpu().numpy(),
+                               r.expert_offsets.cpu().numpy(), qw, sc)
+    assert v["ok"], v
+
+
+@pytest.mark.parametrize("T", [4, 300])
+def test_malformed_lists_stay_in_bounds(dev, T):
+    """Lists out of range are clamped: anything may come out, nothing faults.  The
+    buffers stand between guard words."""
+    E, topk, F, K = 4, 2, 32, 64
+    R = T * topk
+    rng = np.random.default_rng(6)
+    Xd, _ = activations(rng, T, K, "bf16")
+    qwd, scd = on(dev, *weights_of(rng, E, 2 * F, K))
+    tok = torch.randint(-5, 2 * T, (R,), dtype=torch.int32, device=dev)
+    off = torch.tensor([-3, R + 9, 1, R // 2, 7 * R], dtype=torch.int32, device=dev)
+    buf = torch.full((R * F + 512,), 77.0, dtype=torch.bfloat16, device=dev)
+    pkg.w4a16_gemm_grouped_swiglu(Xd, tok, off, qwd, scd, buf[256:256 + R * F].view(R, F))
+    dq, ds = on(dev, *weights_of(rng, E, F, K))
+    Hd, _ = activations(rng, R, K, "bf16")
+    slots = torch.randint(-9, 2 * R, (T, topk), dtype=torch.int32, device=dev)
+    Y = pkg.w4a16_gemm_grouped_combine(Hd, off, dq, ds, slots, torch.rand(T, topk, device=dev))
+    torch.cuda.synchronize()
+    assert torch.all(buf[:256] == 77) and torch.all(buf[256 + R * F:] == 77)
+    assert Y.shape == (T, F)
+
+
+def test_far_magnitudes(dev):
+    """Activations near the ends of the 16-bit types, zero rows, zero scales."""
+    E, F, K = 2, 20, 96
+    rng = np.random.default_rng(12)
+    for per in (6, 90):  # either kernel
+        tok, off = lists_of([per, per], 8, rng)
+        qw, sc = weights_of(rng, E, 2 * F, K)
+        sc[0, 3] = 0.0
+        for dtype, big in (("fp16", 6e4), ("bf16", 1e15), ("fp32", 1e15)):
+            x = rng.standard_normal((8, K))
+            x[1] = 0.0
+            x[2] *= big / 8
+            x[3] *= 2.0 ** -20
+            sc2 = sc / np.float32(big)  # sums of ordinary size
+            t = torch.from_numpy(x.astype(np.float32)).to(TYPES[dtype])
+            tokd, offd, qwd, scd = on(dev, tok, off, qw, sc2)
+            H = pkg.w4a16_gemm_grouped_swiglu(t.to(dev), tokd, offd, qwd, scd)
+            want, tol = oracle.experts_swiglu(t.float().numpy(), tok, off, qw, sc2, dtype)
+            within(H, want, tol, f"far {dtype} {per}")
+
+
+def test_binding_refusals(dev):
+    r = pkg.w4a16_moe_route(torch.randn(4, 8, device=dev), 2)
+    X = torch.randn(4, 64, device=dev)
+    qw = torch.zeros(8, 32, 8, dtype=torch.int32, device=dev)
+    sc = torch.ones(8, 32, 2, device=dev)
+    ok = pkg.w4a16_gemm_grouped_swiglu(X, r.token_index, r.expert_offsets, qw, sc)
+    assert ok.shape == (8, 16)
+    with pytest.raises(TypeError):
+        pkg.w4a16_gemm_grouped_swiglu(X.double(), r.token_index, r.expert_offsets, qw, sc)
+    with pytest.raises(TypeError):
+        pkg.w4a16_gemm_grouped_swiglu(X, r.token_index.long(), r.expert_offsets, qw, sc)
+    with pytest.raises(ValueError):
+        pkg.w4a16_gemm_grouped_swiglu(X, r.token_index, r.expert_offsets[:-1], qw, sc)
+    with pytest.raises(ValueError):
+        pkg.w4a16_gemm_grouped_swiglu(X, r.token_index, r.expert_offsets, qw[:, :31].contiguous(),
+                                      sc[:, :31].contiguous())
+    with pytest.raises(ValueError):
+        pkg.w4a16_gemm_grouped_swiglu(X.t(), r.token_index, r.expert_offsets, qw, sc)
+    with pytest.raises(TypeError):  # H in another type than X
+        pkg.w4a16_gemm_grouped_swiglu(X, r.token_index, r.expert_offsets, qw, sc, ok.half())
+    with pytest.raises(ValueError):  # 4 tokens take 8 rows
+        pkg.w4a16_gemm_grouped_combine(X, r.expert_offsets, qw, sc, r.slots, r.weights)
+    with pytest.raises(ValueError):
+        pkg.w4a16_moe_route(torch.randn(4, 8, device=dev), 2, bias=torch.zeros(7, device=dev))
+    with pytest.raises(ValueError):
+        pkg.w4a16_moe_route(torch.randn(4, 8, device=dev), 2, score="max")
+    for bad in (dict(topk=9), dict(topk=0), dict(topk=2, groups=3), dict(topk=2, group_limit=2)):
+        with pytest.raises(pkg.W4A16Error):
+            pkg.w4a16_moe_route(torch.randn(4, 8, device=dev), **bad)
