@@ -492,7 +492,7 @@ int w4a16_gemm_split_packed(const float *X, const void *packed, float *Y, int64_
 #define W4A16_ROUTE_MAX_TOPK 32
 #define W4A16_ROUTE_MAX_GROUPS 64
 
-/* Workspace bytes of w4a16_moe_route (0 up to 64 tokens, or for extents it
+/* Workspace bytes of w4a16_moe_route (0 up to 16 tokens, or for extents it
  * refuses).  Host only. */
 size_t w4a16_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t topk);
 
@@ -510,7 +510,7 @@ size_t w4a16_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t topk);
  * logits; key c_e = s_e + bias_e.  With group_limit < groups, experts are
  * taken from group_limit of `groups` runs of E / groups neighbouring experts
  * only: a group is worth the sum of its group_top (1 or 2) largest keys, and
- * the largest groups stay.  The topk largest keys are chosen.  Ties go to the
+ * the groups of the largest worth stay.  The topk largest keys are chosen.  Ties go to the
  * lower index.  weights = s of the chosen (divided by their sum if
  * renormalize is not 0; 0 if that sum is 0) times scale.  Slots are sorted by
  * expert, then token.
@@ -544,8 +544,8 @@ int w4a16_moe_route(const void *logits, const float *bias, const int32_t *num_to
  * extents that are refused or a no-op.  Host only. */
 int w4a16_experts_kernel(int64_t R, int64_t E);
 
-/* Workspace bytes of w4a16_gemm_grouped_swiglu (0 for the skinny kernel and
- * for extents it refuses).  Host only. */
+/* Workspace bytes of w4a16_gemm_grouped_swiglu (0 for the skinny kernel on
+ * 16-bit activations and for extents it refuses).  Host only. */
 size_t w4a16_grouped_swiglu_workspace_bytes(int64_t T, int64_t R, int64_t E, int64_t F, int64_t K,
                                             int32_t dtype);
 
@@ -561,8 +561,9 @@ size_t w4a16_grouped_swiglu_workspace_bytes(int64_t T, int64_t R, int64_t E, int
  *   qweight         int32 [E][2F][K/8], scales float [E][2F][K/32]
  *   H               [R][F], dtype
  * The weights of an expert without slots are not read.  token_index and
- * expert_offsets are clamped into range on the device.  fp32 activations meet
- * the tolerance of w4a16_gemm on both sums, and so do fp16 ones.  bf16 ones
+ * expert_offsets are clamped into range on the device.  fp32 activations (two
+ * fp16 limbs per row, as w4a16_gemm_split) meet the tolerance of w4a16_gemm on
+ * both sums, and so do fp16 ones.  bf16 ones
  * meet it with scale * |x| * (q + 40) in place of |x * w| (the skinny kernel
  * multiplies by q + 16 and takes 24 off again in fp32); the tile kernel scales
  * them per row into fp16, exactly for values down to 2^-28 of their row's

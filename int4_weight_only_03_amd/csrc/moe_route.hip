@@ -15,9 +15,9 @@
 //
 // The choice is that of 64-bit keys.  Without a bias the scores are in the
 // logits' order, so the logits themselves are compared.  Otherwise a token's
-// keys are computed in fp32 first, with an error below kTol(key); if any two
-// values whose order decides something lie closer than twice that, the token
-// is done again with 64-bit keys (about 1 token in 500 at 256 experts).
+// keys are computed in fp32 first; if any two values whose order decides
+// something lie closer than their errors, the token is done again with 64-bit
+// keys (about 1 token in 1000 at 256 experts).
 //
 // Slots are sorted by expert, then token.  A block of tokens counts its
 // choices per expert; a second kernel sums the blocks before its own and ranks
@@ -25,11 +25,15 @@
 // tokens' choices of an expert are one 64-bit mask, ORed together in LDS (any
 // order gives the same mask), and a choice's rank is a population count: no
 // result depends on the order of atomics.  One block of up to 64 tokens does
-// both in one launch.
+// both in one launch, and one wave does a single token.
 //
-// Bound: at few tokens by launch and load latency; at many by VALU issue of
-// the selection (about 700 instructions a token at 256 experts, top 8 of 4 out
-// of 8 groups).
+// A token is worked on by LP lanes, expert e in register e / LP of lane e % LP:
+// by a whole wave where tokens are few (a pick's chain of dependent reductions
+// is what takes the time), by 16 lanes, four tokens a wave, where they are many
+// (the same instructions serve four tokens).
+//
+// Bound: at few tokens by launch and the picks' latency; at many by VALU issue
+// of the selection.
 
 #include "moe_common.h"
 
@@ -41,8 +45,7 @@ namespace {
 
 constexpr int kRtWaves = 16;
 constexpr int kRtThreads = 64 * kRtWaves;
-constexpr int kRtSingle = 64;     // tokens of the one-launch form
-constexpr int kRtMaxBlocks = 256; // blocks of the first kernel
+constexpr int kRtMaxBlocks = 256; // blocks of the second kernel
 
 struct RouteArgs {
   const void *logits;
@@ -53,233 +56,403 @@ struct RouteArgs {
   int32_t *slots;              // [T][topk]
   int32_t *token_index;        // [T * topk]
   int32_t *offsets;            // [E + 1]
-  int32_t *counts;             // [blocks][E]
-  int T, E, topk, groups, group_limit, group_top, sigmoid, renormalize;
+  int32_t *counts;             // [blocks][padded(E)]
+  int T, E, topk, groups, group_limit, group_top, sigmoid, renormalize, dtype;
   float scale;
-  int chunk, blocks;           // tokens per block, blocks
+  int at_once, blocks;         // the first kernel's tokens per block, blocks
+  int chunk;                   // the second's tokens per block (a multiple of 64)
 };
+
+// row of the counts: a multiple of 4 experts
+__host__ __device__ constexpr int padded(int E) { return (E + 3) & ~3; }
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
-__device__ __forceinline__ float wave_max(float v) {
-  // row shifts 1, 2, 4, 8, then rows 0 and 2 into 1 and 3, then row 1 into 2
-  // and 3: lane 63 holds the maximum (lanes without a source keep their own)
-#define W4A16_RT_STEP(CTRL, ROWS)                                                            \
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(                                   \
-                   __float_as_int(v), __float_as_int(v), CTRL, ROWS, 0xf, false)))
-  W4A16_RT_STEP(0x111, 0xf);
-  W4A16_RT_STEP(0x112, 0xf);
-  W4A16_RT_STEP(0x114, 0xf);
-  W4A16_RT_STEP(0x118, 0xf);
-  W4A16_RT_STEP(0x142, 0xa);
-  W4A16_RT_STEP(0x143, 0xc);
-#undef W4A16_RT_STEP
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
-
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = fmax(v, __shfl_xor(v, d, 64));
-  return v;
-}
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
-}
-
-__device__ __forceinline__ float exp_of(float x) { return expf(x); }
+// fp32: exp2 of the rounded product; the product's rounding is an error of
+// |x| 2^-24 of the result, at most 0.37 * 2^-24 absolute for x <= 0, and so is
+// the instruction's, 2^-23 relative
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
+__device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }  // 1 ulp
+__device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
 
-// Bound of twice the error of a fp32 key or of a sum of two: scores are at
-// most 1 with a relative error below 12 * 2^-24 (exp 1 ulp, the softmax sum of
-// up to 1024 terms in 64 bits, one division), each addition rounds once.
+__device__ __forceinline__ float read_lane(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double read_lane(double v, int lane) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                          __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
+
+// A lane of the other half of this lane's aligned run of 2 D lanes (the xor
+// partner, or for D = 4 and 8 the mirrored lane: the same where each half holds
+// one value throughout, as it does in a butterfly).
+template <int D>
+__device__ __forceinline__ int other_half(int v) {
+  if constexpr (D == 1) {
+    return __builtin_amdgcn_update_dpp(v, v, 0xB1, 0xf, 0xf, false);
+  } else if constexpr (D == 2) {
+    return __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xf, 0xf, false);
+  } else if constexpr (D == 4) {
+    return __builtin_amdgcn_update_dpp(v, v, 0x141, 0xf, 0xf, false);
+  } else if constexpr (D == 8) {
+    return __builtin_amdgcn_update_dpp(v, v, 0x140, 0xf, 0xf, false);
+  } else if constexpr (D == 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(uint32_t(v), uint32_t(v), false, false);
+    return int((threadIdx.x & 16) ? p[0] : p[1]);
+  } else {
+    const auto p = __builtin_amdgcn_permlane32_swap(uint32_t(v), uint32_t(v), false, false);
+    return int((threadIdx.x & 32) ? p[0] : p[1]);
+  }
+}
+template <int D>
+__device__ __forceinline__ float other_half(float v) {
+  return __int_as_float(other_half<D>(__float_as_int(v)));
+}
+template <int D>
+__device__ __forceinline__ double other_half(double v) {
+  return __hiloint2double(other_half<D>(__double2hiint(v)), other_half<D>(__double2loint(v)));
+}
+
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+
+// over a token's LP lanes; every lane gets the result
+template <int LP, typename V>
+__device__ __forceinline__ V token_max(V v) {
+  v = larger(v, other_half<1>(v));
+  v = larger(v, other_half<2>(v));
+  v = larger(v, other_half<4>(v));
+  v = larger(v, other_half<8>(v));
+  if constexpr (LP == 64) {
+    v = larger(v, other_half<16>(v));
+    v = larger(v, other_half<32>(v));
+  }
+  return v;
+}
+template <int LP>
+__device__ __forceinline__ int token_min(int v) {
+  v = min(v, other_half<1>(v));
+  v = min(v, other_half<2>(v));
+  v = min(v, other_half<4>(v));
+  v = min(v, other_half<8>(v));
+  if constexpr (LP == 64) {
+    v = min(v, other_half<16>(v));
+    v = min(v, other_half<32>(v));
+  }
+  return v;
+}
+template <int LP>
+__device__ __forceinline__ double token_sum(double v) {
+  v += other_half<1>(v);
+  v += other_half<2>(v);
+  v += other_half<4>(v);
+  v += other_half<8>(v);
+  if constexpr (LP == 64) {
+    v += other_half<16>(v);
+    v += other_half<32>(v);
+  }
+  return v;
+}
+
+// the value of lane I of this lane's row of 16
+template <int I>
+__device__ __forceinline__ int row_lane(int v) {
+  return __builtin_amdgcn_update_dpp(v, v, 0x150 + I, 0xf, 0xf, false);
+}
+template <int I>
+__device__ __forceinline__ float row_lane(float v) {
+  return __int_as_float(row_lane<I>(__float_as_int(v)));
+}
+template <int I>
+__device__ __forceinline__ double row_lane(double v) {
+  return __hiloint2double(row_lane<I>(__double2hiint(v)), row_lane<I>(__double2loint(v)));
+}
+
+// the two largest values of both halves
+template <int D, typename KT>
+__device__ __forceinline__ void merge_two(KT &m1, KT &m2) {
+  const KT o1 = other_half<D>(m1), o2 = other_half<D>(m2);
+  m2 = o1 > m1 ? (m1 > o2 ? m1 : o2) : (o1 > m2 ? o1 : m2);
+  m1 = o1 > m1 ? o1 : m1;
+}
+
+// Whether fp32 values of `n` scores each lie closer than their errors.  A score
+// is off by at most 5 * 2^-24: sigmoid by s (1 - s) |x| 2^-24 < 0.3 (the
+// exponent's rounding), 0.5 (exp2, 1 ulp of e s^2), 1 (the sum) and 2 (the
+// reciprocal, 1 ulp) of 2^-24 times s; softmax terms by 0.4 + 2, the products
+// and the reciprocal of their sum by 5, times scores that are below 1/2 where
+// two compete.  Each addition rounds once more, in proportion to the value.
 template <typename KT>
-__device__ __forceinline__ bool too_close(KT hi, KT lo) {
+__device__ __forceinline__ bool too_close(KT hi, KT lo, int n) {
   if constexpr (sizeof(KT) == 8) return false;  // 64-bit keys decide as they are
   const float d = float(hi) - float(lo);
-  return !(d > 4e-6f + 1e-6f * fmaxf(fabsf(float(hi)), fabsf(float(lo))));
+  return !(d > float(n) * (12 * 0x1p-24f + 4 * 0x1p-24f * fmaxf(fabsf(float(hi)), fabsf(float(lo)))));
 }
 
-template <int NV>
-struct Token {
-  float x[NV];      // logits of experts 64 r + lane; masked ones -inf
-  float chosen_x;   // lane j: logit of the j-th choice
-  int chosen;       // lane j: its expert, -1 where none
+// Rank of a group of value `value` among a token's: h runs over the groups, g is
+// its own index.  Group g is held by lanes g L .. g L + L - 1 of the token's.
+template <typename KT>
+__device__ __forceinline__ int above(KT v, int h, KT value, int g) {
+  return (v > value || (v == value && h < g)) ? 1 : 0;
+}
+template <int I, typename KT>
+__device__ __forceinline__ void rank_row(KT value, int g, int L, int groups, int &rank) {
+  if ((I & (L - 1)) == 0 && I < groups * L)  // uniform
+    rank += above(row_lane<I>(value), I / L, value, g);
+  if constexpr (I < 15) rank_row<I + 1>(value, g, L, groups, rank);
+}
+
+// The logits of up to 64 tokens that threads work on together: row t - first of
+// them starts at base + (t - first) * E elements.  Reads past the last row give
+// 0 (and are masked), so a lane needs no clamp and its reads differ in constants.
+struct Rows {
+  const char *base;  // uniform
+  uint32_t bytes;    // of all the rows
+  uint32_t at;       // this lane's token's row, elements
+  int E, dtype;
 };
 
-// Order the token's experts by keys of type KT; returns false if fp32 cannot
-// tell.  kBias: keys are s + b, else the logits.  keys: this wave's LDS room
-// for E values (used with groups only).  top: largest logit, sum: sum of
-// exp(l - top) (softmax).
-template <typename KT, int NV, bool kBias>
-__device__ __forceinline__ bool select_experts(const RouteArgs &a, Token<NV> &tk,
-                                               const float (&b)[NV], const int (&grp)[NV],
-                                               float top, double sum, KT *keys) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, int(bytes), 0x00027000);
+}
+
+// logits of experts r LP + l, masked ones (NaN, -inf, none there, token not
+// live) -inf
+template <int LP, int NV>
+__device__ __forceinline__ void load_logits(const Rows &w, bool live, float (&x)[NV]) {
+  const int l = threadIdx.x & (LP - 1);
+  const __amdgpu_buffer_rsrc_t rs = resource(w.base, w.bytes);
+  const uint32_t at = w.at + uint32_t(l);
+  if (w.dtype == W4A16_DTYPE_F32) {
+#pragma unroll
+    for (int r = 0; r < NV; ++r)
+      x[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, int(at * 4) + r * LP * 4, 0, 0));
+  } else {
+    uint16_t h[NV];
+#pragma unroll
+    for (int r = 0; r < NV; ++r)
+      h[r] = __builtin_amdgcn_raw_buffer_load_b16(rs, int(at * 2) + r * LP * 2, 0, 0);
+#pragma unroll
+    for (int r = 0; r < NV; ++r)
+      x[r] = w.dtype == W4A16_DTYPE_F16 ? float(__builtin_bit_cast(_Float16, h[r]))
+                                        : __uint_as_float(uint32_t(h[r]) << 16);
+  }
+#pragma unroll
+  for (int r = 0; r < NV; ++r)
+    x[r] = (live && r * LP + l < w.E && x[r] > kNegInf) ? x[r] : kNegInf;
+}
+
+__device__ __forceinline__ float load_logit(const Rows &w, int e) {
+  const __amdgpu_buffer_rsrc_t rs = resource(w.base, w.bytes);
+  const uint32_t at = w.at + uint32_t(e);
+  if (w.dtype == W4A16_DTYPE_F32)
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, int(at * 4), 0, 0));
+  const uint16_t h = __builtin_amdgcn_raw_buffer_load_b16(rs, int(at * 2), 0, 0);
+  return w.dtype == W4A16_DTYPE_F16 ? float(__builtin_bit_cast(_Float16, h))
+                                    : __uint_as_float(uint32_t(h) << 16);
+}
+
+// What a token's selection needs of the call.
+struct Select {
+  const float *bias;
+  int topk, groups, group_limit, group_top;
+};
+
+// Order a token's experts by keys of type KT; false on a lane of a token that
+// fp32 cannot tell.  kBias: keys are s + b, else the logits.  keys: the token's
+// LDS room of LP * NV values (used with groups only).  top: largest logit, sum:
+// sum of exp(l - top) (softmax).  Lane j of the token leaves with its j-th
+// choice, -1 where none.
+template <typename KT, int LP, int NV, bool kBias, bool kSigmoid>
+__device__ __forceinline__ bool select_experts(const Select &a, int E, const float (&x)[NV],
+                                               float top, double sum, KT *keys, int &chosen) {
+  const int l = threadIdx.x & (LP - 1);
   const bool grouped = a.group_limit < a.groups;
+  // groups are valued by the keys, or by the scores where two are added
+  const bool scores = kBias || (grouped && a.group_top == 2);
   const KT low = KT(kNegInf);
   KT key[NV];
-  KT gkey[NV];  // what groups are valued by
 #pragma unroll
-  for (int r = 0; r < NV; ++r) {
-    const float x = tk.x[r];
-    key[r] = KT(x);
-    gkey[r] = key[r];
-    if (kBias || grouped) {
-      KT s;
-      if (a.sigmoid)
-        s = KT(1) / (KT(1) + exp_of(-KT(x)));
-      else
-        s = (x == top ? KT(1) : exp_of(KT(x) - KT(top))) / KT(sum);
-      if (kBias) {
-        s += KT(b[r]);
-        if (!(s > low)) s = low;  // a NaN or -inf bias masks
-        key[r] = x > kNegInf ? s : low;
-      }
-      gkey[r] = x > kNegInf ? s : low;
+  for (int r = 0; r < NV; ++r) key[r] = KT(x[r]);
+  if (scores) {
+    KT value[NV];
+    const KT over = kSigmoid ? KT(1) : inverse(KT(sum));
+#pragma unroll
+    for (int r = 0; r < NV; ++r) {
+      const KT p = exp_of(kSigmoid ? -KT(x[r]) : KT(x[r]) - KT(top));
+      value[r] = kSigmoid ? inverse(KT(1) + p) : (x[r] == top ? KT(1) : p) * over;
     }
+    if constexpr (kBias) {
+      const __amdgpu_buffer_rsrc_t rs = resource(a.bias, uint32_t(E) * 4u);
+      float b[NV];
+#pragma unroll
+      for (int r = 0; r < NV; ++r)
+        b[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, 4 * l + r * LP * 4, 0, 0));
+#pragma unroll
+      for (int r = 0; r < NV; ++r) {
+        value[r] += KT(b[r]);
+        value[r] = value[r] > low ? value[r] : low;  // a NaN or -inf bias masks
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < NV; ++r) {
+      value[r] = x[r] > kNegInf ? value[r] : low;
+      if (kBias) key[r] = value[r];
+    }
+    if (grouped) {
+#pragma unroll
+      for (int r = 0; r < NV; ++r) keys[r * LP + l] = value[r];
+    }
+  } else if (grouped) {
+#pragma unroll
+    for (int r = 0; r < NV; ++r) keys[r * LP + l] = key[r];
   }
   bool sure = true;
   if (grouped) {
-    // groups side by side: 64 / groups lanes (a power of two) per group, each
-    // taking every L-th of its experts, the two largest merged across them
-    const int L = 1 << (31 - __clz(64 / a.groups));
-    const int gs = a.E / a.groups;
-    const int g = lane / L;
-#pragma unroll
-    for (int r = 0; r < NV; ++r)
-      if (64 * r + lane < a.E) keys[64 * r + lane] = gkey[r];
+    // groups side by side, L lanes (a power of two) each, a lane taking every
+    // L-th of the group's experts; the two largest are merged across them
+    const int L = 1 << (31 - __clz(LP / a.groups));
+    const int gs = E / a.groups;
+    const int g = l / L;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     KT m1 = low, m2 = low;
     if (g < a.groups)
-      for (int i = lane - g * L; i < gs; i += L) {
+      for (int i = l - g * L; i < gs; i += L) {
         const KT v = keys[g * gs + i];
         m2 = v > m1 ? m1 : (v > m2 ? v : m2);
         m1 = v > m1 ? v : m1;
       }
-    for (int d = 1; d < L; d <<= 1) {
-      const KT o1 = __shfl_xor(m1, d, 64), o2 = __shfl_xor(m2, d, 64);
-      m2 = o1 > m1 ? (m1 > o2 ? m1 : o2) : (o1 > m2 ? o1 : m2);
-      m1 = o1 > m1 ? o1 : m1;
-    }
+    if (L > 1) merge_two<1>(m1, m2);
+    if (L > 2) merge_two<2>(m1, m2);
+    if (L > 4) merge_two<4>(m1, m2);
+    if (L > 8) merge_two<8>(m1, m2);
+    if (LP == 64 && L > 16) merge_two<16>(m1, m2);
+    if (LP == 64 && L > 32) merge_two<32>(m1, m2);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // before the room is written again
     __builtin_amdgcn_wave_barrier();
     KT value = m1;
     if (a.group_top == 2 && m2 > low) value += m2;
     int rank = 0;
-    bool near = false;
-    for (int h = 0; h < a.groups; ++h) {
-      const KT v = __shfl(value, h * L, 64);
-      rank += (v > value || (v == value && h < g)) ? 1 : 0;
-      near |= h != g && m1 > low && v > low && too_close(v > value ? v : value, v > value ? value : v);
+    if constexpr (LP == 64) {
+      for (int h = 0; h < a.groups; ++h) rank += above(read_lane(value, h * L), h, value, g);
+    } else {
+      rank_row<0>(value, g, L, a.groups, rank);
     }
-    const unsigned long long kept =
-        __ballot(g < a.groups && m1 > low && rank < a.group_limit);
-    sure = __ballot(near && g < a.groups) == 0;
+    const bool open = g < a.groups && m1 > low, keep = open && rank < a.group_limit;
+    const unsigned long long kept = __ballot(keep) >> ((threadIdx.x & 63) & ~(LP - 1));
+    if (scores) {  // the least of the kept against the largest of the others
+      const KT least = -token_max<LP>(keep ? -value : low);
+      const KT most = token_max<LP>(open && !keep ? value : low);
+      sure = !(most > low && too_close(least, most, a.group_top));
+    }
+    // e / gs = (e * ceil(2^20 / gs)) >> 20 for e < 1024 (gs < 1024: two groups
+    // at least)
+    const uint32_t over_gs = ((1u << 20) + uint32_t(gs) - 1) / uint32_t(gs);
 #pragma unroll
-    for (int r = 0; r < NV; ++r)
-      if (!((kept >> (grp[r] * L)) & 1)) key[r] = low;
+    for (int r = 0; r < NV; ++r) {
+      const uint32_t of = (uint32_t(r * LP + l) * over_gs) >> 20;
+      key[r] = ((kept >> ((of * L) & 63)) & 1) ? key[r] : low;
+    }
   }
   // topk + 1 picks: the last shows how near the first one left out comes
-  tk.chosen = -1;
-  tk.chosen_x = 0.0f;
+  chosen = -1;
   KT last = low;
   for (int j = 0; j <= a.topk; ++j) {
     KT m = key[0];
 #pragma unroll
-    for (int r = 1; r < NV; ++r) m = key[r] > m ? key[r] : m;
-    m = wave_max(m);
-    if (!(m > low)) break;
-    if (kBias && j > 0 && too_close(last, m)) sure = false;
+    for (int r = 1; r < NV; ++r) m = larger(m, key[r]);
+    m = token_max<LP>(m);
+    if (kBias && j > 0 && m > low && too_close(last, m, 1)) sure = false;
     last = m;
     if (j == a.topk) break;
-    bool done = false;
+    int at = 0x7fffffff;  // the lowest expert that has it
 #pragma unroll
-    for (int r = 0; r < NV; ++r) {
-      const unsigned long long at = __ballot(key[r] == m);
-      if (!done && at != 0) {
-        const int l = __builtin_ctzll(at);
-        const float x =
-            __int_as_float(__builtin_amdgcn_readlane(__float_as_int(tk.x[r]), l));
-        if (lane == j) {
-          tk.chosen = 64 * r + l;
-          tk.chosen_x = x;
-        }
-        if (lane == l) key[r] = low;
-        done = true;
-      }
-    }
+    for (int r = NV - 1; r >= 0; --r) at = key[r] == m ? r * LP + l : at;
+    at = token_min<LP>(at);
+#pragma unroll
+    for (int r = 0; r < NV; ++r) key[r] = at - l == r * LP ? low : key[r];
+    if (l == j && m > low) chosen = at;
   }
   return sure;
 }
 
-// One token by one wave: lane j < topk leaves with its j-th choice and weight.
-template <typename LT, int NV, bool kBias>
-__device__ __forceinline__ void route_token(const RouteArgs &a, int t, const float (&b)[NV],
-                                            const int (&grp)[NV], double *keys, int &id,
-                                            float &weight) {
-  const int lane = threadIdx.x & 63;
-  const LT *row = static_cast<const LT *>(a.logits) + long(t) * a.E;
-  Token<NV> tk;
+// The selection in 64 bits: out of line, taken by few waves.
+template <int LP, int NV, bool kBias, bool kSigmoid>
+__device__ __noinline__ int select_64(Rows w, Select a, bool live, float top, double *keys) {
+  // what is uniform comes in vector registers
+  w.base = reinterpret_cast<const char *>(
+      uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(uint64_t(w.base))))) |
+      uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(uint64_t(w.base) >> 32)))) << 32);
+  a.bias = reinterpret_cast<const float *>(
+      uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(uint64_t(a.bias))))) |
+      uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(uint64_t(a.bias) >> 32)))) << 32);
+  w.bytes = uint32_t(__builtin_amdgcn_readfirstlane(int(w.bytes)));
+  w.E = __builtin_amdgcn_readfirstlane(w.E);
+  w.dtype = __builtin_amdgcn_readfirstlane(w.dtype);
+  a.topk = __builtin_amdgcn_readfirstlane(a.topk);
+  a.groups = __builtin_amdgcn_readfirstlane(a.groups);
+  a.group_limit = __builtin_amdgcn_readfirstlane(a.group_limit);
+  a.group_top = __builtin_amdgcn_readfirstlane(a.group_top);
+  float x[NV];
+  load_logits<LP, NV>(w, live, x);
+  double sum = 0.0;
+  if constexpr (!kSigmoid) {
 #pragma unroll
-  for (int r = 0; r < NV; ++r) {
-    const int e = 64 * r + lane;
-    const float x = to_f32(row[min(e, a.E - 1)]);
-    tk.x[r] = (e < a.E && x > kNegInf) ? x : kNegInf;  // a NaN is masked too
+    for (int r = 0; r < NV; ++r) {
+      const double p = exp(double(x[r]) - double(top));
+      sum += x[r] == top ? 1.0 : p;
+    }
+    sum = token_sum<LP>(sum);
   }
+  int id;
+  select_experts<double, LP, NV, kBias, kSigmoid>(a, w.E, x, top, sum, keys, id);
+  return id;
+}
+
+// A token by LP lanes: lane j < topk leaves with its j-th choice and weight.
+// Every token of the wave takes part, those that are not there (live false)
+// with every expert masked.
+template <int LP, int NV, bool kBias, bool kSigmoid>
+__device__ __forceinline__ void route_token(const RouteArgs &a, const Rows &w, bool live,
+                                            double *keys, int &id, float &weight) {
+  const Select sel = {a.bias, a.topk, a.groups, a.group_limit, a.group_top};
+  float x[NV];
+  load_logits<LP, NV>(w, live, x);
   const bool grouped = a.group_limit < a.groups;
+  const bool scores = kBias || (grouped && a.group_top == 2);
   float top = 0.0f;
   double sum = 1.0;
-  if (!a.sigmoid) {
-    float m = tk.x[0];
+  if constexpr (!kSigmoid) {
+    float m = x[0];
 #pragma unroll
-    for (int r = 1; r < NV; ++r) m = fmaxf(m, tk.x[r]);
-    top = wave_max(m);
-    if (kBias || grouped || !a.renormalize) {
+    for (int r = 1; r < NV; ++r) m = fmaxf(m, x[r]);
+    top = token_max<LP>(m);
+    if (scores || !a.renormalize) {
       // fp32 terms summed in 64 bits: the error of the sum is the terms' own
       double s = 0.0;
 #pragma unroll
-      for (int r = 0; r < NV; ++r)
-        s += tk.x[r] > kNegInf ? (tk.x[r] == top ? 1.0 : double(expf(tk.x[r] - top))) : 0.0;
-      sum = wave_sum(s);
+      for (int r = 0; r < NV; ++r) {
+        const float p = expf(x[r] - top);
+        s += double(x[r] == top ? 1.0f : p);
+      }
+      sum = token_sum<LP>(s);
     }
   }
-  bool sure;
-  if constexpr (!kBias) {
-    sure = select_experts<float, NV, false>(a, tk, b, grp, top, sum,
-                                            reinterpret_cast<float *>(keys));
-  } else {
-    sure = select_experts<float, NV, true>(a, tk, b, grp, top, sum,
-                                           reinterpret_cast<float *>(keys));
-  }
-  if (!sure) {  // uniform over the wave
-    if (!a.sigmoid) {
-      double s = 0.0;
-#pragma unroll
-      for (int r = 0; r < NV; ++r)
-        s += tk.x[r] > kNegInf ? (tk.x[r] == top ? 1.0 : exp(double(tk.x[r]) - double(top))) : 0.0;
-      sum = wave_sum(s);
-    }
-    select_experts<double, NV, kBias>(a, tk, b, grp, top, sum, keys);
-  }
+  const bool sure = select_experts<float, LP, NV, kBias, kSigmoid>(
+      sel, w.E, x, top, sum, reinterpret_cast<float *>(keys), id);
+  if (__ballot(!sure) != 0) id = select_64<LP, NV, kBias, kSigmoid>(w, sel, live, top, keys);
   // the chosen scores, one per lane, in 64 bits (a score of 1e-40 still has a
   // share of the chosen ones' sum)
-  double s = 0.0;
-  if (tk.chosen >= 0) {
-    const double x = tk.chosen_x;
-    if (a.sigmoid)
-      s = 1.0 / (1.0 + exp(-x));
-    else
-      s = (tk.chosen_x == top ? 1.0 : exp(x - double(top))) / sum;
-  }
+  const float c = load_logit(w, max(id, 0));
+  const double p = exp(kSigmoid ? -double(c) : double(c) - double(top));
+  double s = kSigmoid ? 1.0 / (1.0 + p) : (c == top ? 1.0 : p) / sum;
+  s = id >= 0 ? s : 0.0;
   if (a.renormalize) {
-    const double all = wave_sum(s);
+    const double all = token_sum<LP>(s);
     s = all > 0.0 ? s / all : 0.0;
   }
-  id = tk.chosen;
   weight = float(s * double(a.scale));
 }
 
@@ -287,31 +460,28 @@ __device__ __forceinline__ int live_tokens(const RouteArgs &a) {
   return a.num_tokens ? min(max(*a.num_tokens, 0), a.T) : a.T;
 }
 
-// Choices of this block's tokens [t0, t1), into memory and, if kept, into LDS.
-template <typename LT, int NV, bool kBias>
-__device__ __forceinline__ void route_tokens(const RouteArgs &a, int t0, int t1, double *keys,
+// Choices of tokens [t0, t0 + n), n <= kRtThreads / LP, into memory and, if
+// kept, into LDS.
+template <int LP, int NV, bool kBias, bool kSigmoid>
+__device__ __forceinline__ void route_tokens(const RouteArgs &a, int t0, int n, double *keys,
                                              int32_t *kept, int *hist) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int live = live_tokens(a);
-  float b[NV];
-  int grp[NV];
-#pragma unroll
-  for (int r = 0; r < NV; ++r) {
-    const int e = min(64 * r + lane, a.E - 1);
-    b[r] = kBias ? a.bias[e] : 0.0f;
-    grp[r] = e / (a.E / a.groups);
-  }
-  double *mine = keys + long(wave) * (a.group_limit < a.groups ? a.E : 0);
-  for (int t = t0 + wave; t < t1; t += kRtWaves) {
-    int id = -1;
-    float w = 0.0f;
-    if (t < live) route_token<LT, NV, kBias>(a, t, b, grp, mine, id, w);
-    if (lane < a.topk) {
-      a.ids[long(t) * a.topk + lane] = id;
-      a.weights[long(t) * a.topk + lane] = w;
-      if (kept) kept[(t - t0) * a.topk + lane] = id;
-      if (hist && id >= 0) atomicAdd(&hist[id], 1);
-    }
+  const int l = threadIdx.x & (LP - 1), mine = threadIdx.x / LP, t = t0 + mine;
+  double *room = keys + (a.group_limit < a.groups ? mine * LP * NV : 0);
+  const int size = a.dtype == W4A16_DTYPE_F32 ? 4 : 2;
+  Rows w;
+  w.base = static_cast<const char *>(a.logits) + long(t0) * a.E * size;
+  w.bytes = uint32_t(n) * uint32_t(a.E) * uint32_t(size);
+  w.at = uint32_t(mine) * uint32_t(a.E);
+  w.E = a.E;
+  w.dtype = a.dtype;
+  int id = -1;
+  float weight = 0.0f;
+  route_token<LP, NV, kBias, kSigmoid>(a, w, mine < n && t < live_tokens(a), room, id, weight);
+  if (mine < n && l < a.topk) {
+    a.ids[long(t) * a.topk + l] = id;
+    a.weights[long(t) * a.topk + l] = weight;
+    if (kept) kept[mine * a.topk + l] = id;
+    if (hist && id >= 0) atomicAdd(&hist[id], 1);
   }
 }
 
@@ -361,34 +531,72 @@ __device__ __forceinline__ void place_choices(const RouteArgs &a, int t0, int n,
   if (tid < a.E) base[tid] += __popcll(mask[tid]);
 }
 
-// LDS: masks [E], then the per-wave keys, then base [E + 1], part, the kept
+// LDS: masks [E], then `keys` of the tokens, then base [E + 1], part, the kept
 // choices (one-launch form).
-__host__ __device__ constexpr size_t route_lds(int E, bool grouped, int kept) {
-  return size_t(E) * 8 + (grouped ? size_t(kRtWaves) * E * 8 : 0) +
-         (size_t(E) + 1 + kRtWaves + kept) * 4;
+__host__ __device__ constexpr size_t route_lds(int E, int keys, int kept) {
+  return size_t(E) * 8 + size_t(keys) * 8 + (size_t(E) + 1 + kRtWaves + kept) * 4;
 }
 
-// kSingle: T <= 64, choices and lists.  Otherwise block b routes tokens
-// [b chunk, (b + 1) chunk) and writes its counts.
-template <typename LT, int NV, bool kBias, bool kSingle>
+// One token: its choices in the order of the experts are the slots, so a choice's
+// slot is the number of chosen experts before its own; one wave, no barrier.
+template <int NV, bool kBias, bool kSigmoid>
+__global__ void __launch_bounds__(64) route_one(RouteArgs a) {
+  extern __shared__ __align__(16) unsigned char rt_lds[];
+  const int lane = threadIdx.x;
+  const int size = a.dtype == W4A16_DTYPE_F32 ? 4 : 2;
+  const Rows row = {static_cast<const char *>(a.logits), uint32_t(a.E) * uint32_t(size), 0, a.E,
+                    a.dtype};
+  int id = -1;
+  float w = 0.0f;
+  route_token<64, NV, kBias, kSigmoid>(a, row, live_tokens(a) > 0,
+                                       reinterpret_cast<double *>(rt_lds), id, w);
+  int slot = 0, n = 0;
+  int start[NV + 1];  // chosen experts before 64 r + lane (the last: before 64 NV, lane 0)
+#pragma unroll
+  for (int r = 0; r <= NV; ++r) start[r] = 0;
+  for (int j = 0; j < a.topk; ++j) {
+    const int other = __builtin_amdgcn_readlane(id, j);
+    if (other < 0) break;  // nor is there any behind it
+    ++n;
+    slot += other < id ? 1 : 0;
+#pragma unroll
+    for (int r = 0; r <= NV; ++r) start[r] += other < 64 * r + lane ? 1 : 0;
+  }
+  if (lane < a.topk) {
+    a.ids[lane] = id;
+    a.weights[lane] = w;
+    a.slots[lane] = id < 0 ? -1 : slot;
+    if (id >= 0) a.token_index[slot] = 0;
+    if (lane >= n) a.token_index[lane] = -1;
+  }
+#pragma unroll
+  for (int r = 0; r <= NV; ++r)
+    if (64 * r + lane <= a.E) a.offsets[64 * r + lane] = start[r];
+}
+
+// Block b routes tokens [b kAtOnce, (b + 1) kAtOnce) and writes its counts.
+// kSingle: there is one block, which builds the lists too.
+template <int LP, int NV, bool kBias, bool kSigmoid, bool kSingle>
 __global__ void __launch_bounds__(kRtThreads) route_choose(RouteArgs a) {
   extern __shared__ __align__(16) unsigned char rt_lds[];
+  constexpr int kAtOnce = kRtThreads / LP;
   const bool grouped = a.group_limit < a.groups;
   auto *mask = reinterpret_cast<unsigned long long *>(rt_lds);
   auto *keys = reinterpret_cast<double *>(mask + a.E);
-  auto *base = reinterpret_cast<int *>(keys + (grouped ? kRtWaves * a.E : 0));
+  auto *base = reinterpret_cast<int *>(keys + (grouped ? kRtThreads * NV : 0));
   const int tid = threadIdx.x;
-  const int t0 = blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
+  const int t0 = blockIdx.x * kAtOnce, n = min(kAtOnce, a.T - t0);
   if (tid < a.E) base[tid] = 0;
   __syncthreads();
   if constexpr (!kSingle) {
-    route_tokens<LT, NV, kBias>(a, t0, t1, keys, nullptr, base);
+    route_tokens<LP, NV, kBias, kSigmoid>(a, t0, n, keys, nullptr, base);
     __syncthreads();
-    if (tid < a.E) a.counts[long(blockIdx.x) * a.E + tid] = base[tid];
+    const int row = padded(a.E);
+    if (tid < row) a.counts[long(blockIdx.x) * row + tid] = tid < a.E ? base[tid] : 0;
   } else {
     int *part = base + a.E + 1;
     int32_t *kept = part + kRtWaves;
-    route_tokens<LT, NV, kBias>(a, t0, t1, keys, kept, base);
+    route_tokens<LP, NV, kBias, kSigmoid>(a, t0, n, keys, kept, base);
     __syncthreads();
     scan_experts(base, a.E, part);
     for (int e = tid; e <= a.E; e += kRtThreads) a.offsets[e] = base[e];
@@ -398,31 +606,48 @@ __global__ void __launch_bounds__(kRtThreads) route_choose(RouteArgs a) {
   }
 }
 
-// Block b: slots of tokens [b chunk, (b + 1) chunk) from the counts.
+// Block b: slots of tokens [b chunk, (b + 1) chunk) from the counts of the first
+// kernel's `blocks` blocks of at_once tokens.
 __global__ void __launch_bounds__(kRtThreads) route_lists(RouteArgs a) {
   extern __shared__ __align__(16) unsigned char rt_lds[];
-  auto *mask = reinterpret_cast<unsigned long long *>(rt_lds);
-  auto *total = reinterpret_cast<int *>(mask + a.E);  // [E + 1]
-  int *before = total + a.E + 1;                      // [E]
-  int *part = before + a.E;                           // [kRtWaves]
+  const int row = padded(a.E);
+  auto *mask = reinterpret_cast<unsigned long long *>(rt_lds);  // [E]
+  auto *total = reinterpret_cast<int *>(mask + a.E);            // [row + 1]
+  int *before = total + row + 1;                                // [row]
+  int *part = before + row;                                     // [kRtWaves]
   const int tid = threadIdx.x;
-  if (tid < a.E) total[tid] = before[tid] = 0;
+  const int first = int(blockIdx.x) * (a.chunk / a.at_once);  // block of its first token
+  if (tid < row) total[tid] = before[tid] = 0;
   __syncthreads();
-  // experts side by side, the blocks dealt to the thread groups that are left
-  int width = 64;
-  while (width < a.E) width <<= 1;
-  const int e = tid & (width - 1);
-  if (e < a.E) {
-    int all = 0, mine = 0;
+  // four experts a thread side by side, the blocks dealt to the thread groups
+  // that are left, all of a group's loads in flight
+  int width = 16;
+  while (4 * width < row) width <<= 1;
+  const int e = 4 * (tid & (width - 1));
+  if (e < row) {
+    int4 all = make_int4(0, 0, 0, 0), mine = all;
     const int step = kRtThreads / width;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = tid / width; k < a.blocks; k += step) {
-      const int c = a.counts[long(k) * a.E + e];
-      all += c;
-      if (k < int(blockIdx.x)) mine += c;
+      const int4 c = *reinterpret_cast<const int4 *>(a.counts + long(k) * row + e);
+      const int own = k < first ? -1 : 0;
+      all.x += c.x;
+      all.y += c.y;
+      all.z += c.z;
+      all.w += c.w;
+      mine.x += c.x & own;
+      mine.y += c.y & own;
+      mine.z += c.z & own;
+      mine.w += c.w & own;
     }
-    atomicAdd(&total[e], all);
-    atomicAdd(&before[e], mine);
+    atomicAdd(&total[e], all.x);
+    atomicAdd(&total[e + 1], all.y);
+    atomicAdd(&total[e + 2], all.z);
+    atomicAdd(&total[e + 3], all.w);
+    atomicAdd(&before[e], mine.x);
+    atomicAdd(&before[e + 1], mine.y);
+    atomicAdd(&before[e + 2], mine.z);
+    atomicAdd(&before[e + 3], mine.w);
   }
   __syncthreads();
   scan_experts(total, a.E, part);
@@ -430,7 +655,7 @@ __global__ void __launch_bounds__(kRtThreads) route_lists(RouteArgs a) {
     for (int i = tid; i <= a.E; i += kRtThreads) a.offsets[i] = total[i];
   const long R = long(a.T) * a.topk;
   for (long r = total[a.E] + long(blockIdx.x) * kRtThreads + tid; r < R;
-       r += long(a.blocks) * kRtThreads)
+       r += long(gridDim.x) * kRtThreads)
     a.token_index[r] = -1;
   if (tid < a.E) before[tid] += total[tid];
   const int t0 = blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.T);
@@ -438,62 +663,70 @@ __global__ void __launch_bounds__(kRtThreads) route_lists(RouteArgs a) {
     place_choices(a, t, min(64, t1 - t), a.ids + long(t) * a.topk, mask, before);
 }
 
-struct RoutePlan {
-  int chunk, blocks;
-};
-
-// One launch up to 64 tokens; above, blocks of a multiple of 16 tokens (one
-// per wave at a time), at most 256 blocks.
-RoutePlan plan_route(long T) {
-  RoutePlan p;
-  if (T <= kRtSingle) {
-    p.chunk = kRtSingle;
-    p.blocks = 1;
-    return p;
-  }
-  const long per = (T + long(kRtWaves) * kRtMaxBlocks - 1) / (long(kRtWaves) * kRtMaxBlocks);
-  p.chunk = int(per * kRtWaves);
-  p.blocks = int((T + p.chunk - 1) / p.chunk);
-  return p;
+// Lanes per token: four tokens a wave past 16 tokens, while their experts,
+// choices and groups fit 16 lanes.
+int lanes_per_token(long T, int E, int topk, int groups) {
+  return T > 16 && E <= 256 && topk <= 16 && groups <= 16 ? 16 : 64;
 }
 
-template <typename LT, int NV, bool kBias>
+// blocks of the first kernel; one builds the lists as well
+long choose_blocks(long T, int lanes) {
+  const long at_once = kRtThreads / lanes;
+  return std::max((T + at_once - 1) / at_once, 1L);
+}
+
+template <int LP, int NV, bool kBias, bool kSigmoid>
 hipError_t run_route(const RouteArgs &a, hipStream_t stream) {
   const bool grouped = a.group_limit < a.groups;
-  if (a.T <= kRtSingle) {
-    const size_t lds = route_lds(a.E, grouped, a.T * a.topk);
-    hipLaunchKernelGGL((route_choose<LT, NV, kBias, true>), dim3(1), dim3(kRtThreads), lds,
-                       stream, a);
+  if (LP == 64 && a.T == 1) {
+    hipLaunchKernelGGL((route_one<NV, kBias, kSigmoid>), dim3(1), dim3(64),
+                       grouped ? LP * NV * 8 : 0, stream, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((route_choose<LT, NV, kBias, false>), dim3(a.blocks), dim3(kRtThreads),
-                     route_lds(a.E, grouped, 0), stream, a);
+  const int keys = grouped ? kRtThreads * NV : 0;
+  if (a.blocks == 1) {
+    hipLaunchKernelGGL((route_choose<LP, NV, kBias, kSigmoid, true>), dim3(1), dim3(kRtThreads),
+                       route_lds(a.E, keys, a.T * a.topk), stream, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((route_choose<LP, NV, kBias, kSigmoid, false>), dim3(a.blocks),
+                     dim3(kRtThreads), route_lds(a.E, keys, 0), stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const size_t lds = size_t(a.E) * 8 + (2 * size_t(a.E) + 1 + kRtWaves) * 4;
-  hipLaunchKernelGGL(route_lists, dim3(a.blocks), dim3(kRtThreads), lds, stream, a);
+  const size_t lds = size_t(a.E) * 8 + (2 * size_t(padded(a.E)) + 1 + kRtWaves) * 4;
+  hipLaunchKernelGGL(route_lists, dim3((a.T + a.chunk - 1) / a.chunk), dim3(kRtThreads), lds,
+                     stream, a);
   return hipGetLastError();
 }
 
-template <typename LT, int NV>
-hipError_t run_route_bias(const RouteArgs &a, hipStream_t stream) {
-  return a.bias ? run_route<LT, NV, true>(a, stream) : run_route<LT, NV, false>(a, stream);
+template <int LP, int NV>
+hipError_t run_route_keys(const RouteArgs &a, hipStream_t stream) {
+  if (a.bias)
+    return a.sigmoid ? run_route<LP, NV, true, true>(a, stream)
+                     : run_route<LP, NV, true, false>(a, stream);
+  return a.sigmoid ? run_route<LP, NV, false, true>(a, stream)
+                   : run_route<LP, NV, false, false>(a, stream);
 }
 
-template <typename LT>
-hipError_t run_route_type(const RouteArgs &a, hipStream_t stream) {
-  if (a.E <= 64) return run_route_bias<LT, 1>(a, stream);
-  if (a.E <= 128) return run_route_bias<LT, 2>(a, stream);
-  if (a.E <= 256) return run_route_bias<LT, 4>(a, stream);
-  if (a.E <= 512) return run_route_bias<LT, 8>(a, stream);
-  return run_route_bias<LT, 16>(a, stream);
+hipError_t run_route_size(const RouteArgs &a, hipStream_t stream) {
+  if (lanes_per_token(a.T, a.E, a.topk, a.groups) == 16) {
+    if (a.E <= 64) return run_route_keys<16, 4>(a, stream);
+    if (a.E <= 128) return run_route_keys<16, 8>(a, stream);
+    if (a.E <= 192) return run_route_keys<16, 12>(a, stream);
+    return run_route_keys<16, 16>(a, stream);
+  }
+  if (a.E <= 64) return run_route_keys<64, 1>(a, stream);
+  if (a.E <= 256) return run_route_keys<64, 4>(a, stream);
+  if (a.E <= 512) return run_route_keys<64, 8>(a, stream);
+  return run_route_keys<64, 16>(a, stream);
 }
 
 }  // namespace
 
+// the groups are not known here: room for the form with more blocks
 size_t route_workspace_bytes(long T, int E) {
-  const RoutePlan p = plan_route(T);
-  return p.blocks > 1 ? size_t(p.blocks) * E * 4 : 0;
+  const long blocks = choose_blocks(T, 64);
+  return blocks > 1 ? size_t(blocks) * padded(E) * 4 : 0;
 }
 
 hipError_t launch_route(const MoeRoute &r, void *workspace, hipStream_t stream) {
@@ -516,14 +749,12 @@ hipError_t launch_route(const MoeRoute &r, void *workspace, hipStream_t stream) 
   a.sigmoid = r.sigmoid;
   a.renormalize = r.renormalize;
   a.scale = r.scale;
-  const RoutePlan p = plan_route(r.T);
-  a.chunk = p.chunk;
-  a.blocks = p.blocks;
-  switch (r.dtype) {
-    case W4A16_DTYPE_F32: return run_route_type<float>(a, stream);
-    case W4A16_DTYPE_F16: return run_route_type<_Float16>(a, stream);
-    default: return run_route_type<Bf16>(a, stream);
-  }
+  const int lanes = lanes_per_token(r.T, r.E, r.topk, r.groups);
+  a.at_once = kRtThreads / lanes;
+  a.blocks = int(choose_blocks(r.T, lanes));
+  a.chunk = int(64 * ((long(r.T) + 64L * kRtMaxBlocks - 1) / (64L * kRtMaxBlocks)));
+  a.dtype = r.dtype;
+  return run_route_size(a, stream);
 }
 
 }  // namespace w4a16

@@ -13,9 +13,9 @@
 // Arithmetic, on 16x16x32 matrix instructions (A: 16 slots, B: 16 rows of W,
 // K: one group of 32), fp32 accumulation, one fp32 FMA per output and group
 // for the group's scale:
-//   fp32  two fp16 limbs of each activation, scaled by a power of two per slot
-//         and pair of groups, the low limb x2^11 and met by the codes x2^-11
-//         (22 significant bits; every product exact in fp32);
+//   fp32  two fp16 limbs of each activation, from moe_limbs.hip, and the exact
+//         codes q - 8 (every product exact in fp32); the row's power of two is
+//         undone at the store;
 //   fp16  the activations as they are and the exact codes q - 8;
 //   bf16  the activations as they are and q + 16, which two VALU instructions
 //         per pair of codes make: an instruction on a B of -24 throughout gives
@@ -28,10 +28,19 @@
 // group 4 s + R of W row c (64 contiguous bytes of each of 16 rows per
 // instruction); two lane swaps across the four lane rows give it word R of
 // each of the step's 4 groups, its B operand.  Its A operand is k = 8R .. 8R+7
-// of slot c, D holds slots 4R .. 4R+3 of W row c.  A workgroup takes MT x 16
-// slots of one expert by NT x 16 rows of W (gate tiles, then the up tiles of
-// the same outputs); its 8 waves take steps in turn (neighbouring waves read
-// neighbouring bytes) and their sums are added in wave order in LDS.
+// of the slot in tile row c, D holds tile rows 4R .. 4R+3 of W row c.  Slot i
+// of 16 stands in tile row 4 (i % 4) + i / 4, so that up to 4 MR slots fill only
+// the first MR of D's registers and the rest cost no scale FMA.
+//
+// A wave takes MT x 16 (or 4 MR) slots of one expert by NT x 16 rows of W (gate
+// tiles, then the up tiles of the same outputs) over blocks of 16 groups; KW
+// waves of a workgroup share a tile, taking blocks in turn, and their sums are
+// added in wave order in LDS.  The next block's weights fly while a block is
+// worked on.  Its scales come in one load per 16 rows of W and block (64 bytes
+// a row) and pass through the wave's own LDS words: loaded step by step, 16
+// bytes a row, they cost more than the weights (measured on 147 MB in this
+// pattern, loads alone: 22.4 us without scales, 34.8 with them step by step,
+// 27.9 by blocks).
 
 #include "moe_common.h"
 #include "gemv_common.h"
@@ -45,8 +54,9 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
-constexpr int kEsWaves = 8;
+constexpr int kEsWaves = 4;
 constexpr int kEsThreads = 64 * kEsWaves;
+constexpr int kEsBlock = 16;  // groups of a block: 4 steps of 4
 
 // 8 activations x0..x7 in the order x0 x4 x1 x5 x2 x6 x3 x7 (that of the
 // nibble conversions)
@@ -67,134 +77,152 @@ __device__ __forceinline__ bf16x8 nibbles_to_bf16_16(uint32_t w) {
   return __builtin_bit_cast(bf16x8, u32x4m{p0, p1, p2, p3});
 }
 
+// k = 8R .. 8R+7 of one group of one slot: fp32 its two limbs (in the nibble
+// conversion's order), else the activations
 template <typename XT>
-struct XChunk;  // k = 8R .. 8R+7 of one group of one slot
-template <>
-struct XChunk<float> {
-  float4 lo, hi;
-};
-template <>
-struct XChunk<_Float16> {
-  u32x4m v;
-};
-template <>
-struct XChunk<Bf16> {
-  u32x4m v;
+struct XChunk {
+  u32x4m v[sizeof(XT) == 4 ? 2 : 1];
 };
 
 struct ExpertArgs {
-  const void *X;               // [rows][K] activations
+  const void *X;               // rows of ldx values: limbs (fp32) or activations
+  const float *factor;         // 2^-e of a row (fp32)
   const int32_t *token_index;  // slot -> row of X, or null: the slot itself
   const int32_t *offsets;      // [E + 1]
   const uint4 *qw;             // [E][N or 2N][G] groups of 16 bytes
   const float *sc;             // [E][N or 2N][G]
   void *Y;                     // [R][ldy]
-  int rows_x, R, E, N, G, ldy, tiles_n;
+  int rows_x, ldx, R, E, N, G, ldy, tiles_n;
 };
 
-// kSw: W has 2N rows, Y is XT; else Y is fp32.
-template <typename XT, int MT, int NT, int P, bool kSw>
-__global__ void __launch_bounds__(kEsThreads) experts_skinny(ExpertArgs a) {
+__device__ __forceinline__ long row_of(const ExpertArgs &a, int slot) {
+  return a.token_index ? std::min(std::max(a.token_index[slot], 0), a.rows_x - 1) : slot;
+}
+
+// kSw: W has 2N rows, Y is XT; else Y is fp32.  P: steps in flight per wave (2
+// or 4).  kOcc: waves per SIMD.
+template <typename XT, int MT, int MR, int NT, int KW, int P, int kOcc, bool kSw>
+__global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a) {
   constexpr int NO = kSw ? NT / 2 : NT;
+  constexpr int B = MT > 1 ? 16 * MT : 4 * MR;  // slots of an item
   constexpr bool kLimbs = sizeof(XT) == 4;
-  constexpr int kTile = MT * NT * 256;
-  __shared__ __align__(16) float red[kEsWaves * kTile];
-  __shared__ __align__(16) float es_inv[kLimbs ? kEsWaves * 16 * MT : 4];
+  static_assert(MT == 1 || MR == 4, "several slot tiles are full ones");
+  // per wave: a block's scales, row n of the tile at 64 n; at the end the sums
+  constexpr int kTile = MT * MR * NT * 64;
+  constexpr int kWaveLds = KW > 1 && kTile > NT * 256 ? kTile : NT * 256;
+  __shared__ __align__(16) float es_lds[kEsWaves * kWaveLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int c = lane & 15, R = lane >> 4;
-  const int item = int(blockIdx.x / unsigned(a.tiles_n));
-  const int n0 = int(blockIdx.x - unsigned(item) * unsigned(a.tiles_n)) * 16 * NO;
-  const ExpertItem it = find_item(a.offsets, a.E, a.R, 16 * MT, item);
-  if (it.e < 0) return;  // uniform over the workgroup
+  float *mem = es_lds + wave * kWaveLds;
+  const int kw = KW > 1 ? wave % KW : 0;
+  const long tile = long(blockIdx.x) * (kEsWaves / KW) + wave / KW;
+  const int item = int(tile / a.tiles_n);
+  const int n0 = int(tile - long(item) * a.tiles_n) * 16 * NO;
+  const ExpertItem it = find_item(a.offsets, a.E, a.R, B, item);
   const int G = a.G, N = a.N;
-  const long K = long(G) * kGroup;
 
-  // this lane's rows of W (clamped: rows past N are computed and not stored)
-  const uint4 *wrow[NT];
-  const float *srow[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const long n = std::min(n0 + 16 * (t % NO) + c, N - 1) + (kSw && t >= NO ? long(N) : 0);
-    const long row = long(it.e) * (kSw ? 2 * long(N) : long(N)) + n;
-    wrow[t] = a.qw + row * G;
-    srow[t] = a.sc + row * G;
-  }
-  // and of the activations (slots past the item repeat its last)
-  const XT *xrow[MT];
-#pragma unroll
-  for (int u = 0; u < MT; ++u) {
-    const int slot = it.row0 + std::min(16 * u + c, it.rows - 1);
-    long row = slot;
-    if (a.token_index) row = std::min(std::max(a.token_index[slot], 0), a.rows_x - 1);
-    xrow[u] = static_cast<const XT *>(a.X) + row * K + 8 * R;
-  }
-
-  struct Ops {
-    u32x4m w[NT];
-    float4 s[NT];
-    XChunk<XT> x[MT][4];
-  };
-  const int S = G / 4;  // whole steps
-  auto load_x = [&](XChunk<XT> &d, int u, long g) {
-    if constexpr (kLimbs) {
-      const float4 *p = reinterpret_cast<const float4 *>(xrow[u] + g * kGroup);
-      d.lo = p[0];
-      d.hi = p[1];
-    } else {
-      d.v = *reinterpret_cast<const u32x4m *>(xrow[u] + g * kGroup);
-    }
-  };
-  auto load = [&](Ops &o, int s) {
-    const long g = 4 * long(s);
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-      o.w[t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4m *>(wrow[t] + g + R));
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const f32x4u v = *reinterpret_cast<const f32x4u *>(srow[t] + g);
-      o.s[t] = make_float4(v.x, v.y, v.z, v.w);
-    }
-#pragma unroll
-    for (int u = 0; u < MT; ++u)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) load_x(o.x[u][q], u, g + q);
-  };
-  // the step past the whole ones: groups past G read group G - 1 and are
-  // left out of the products
-  auto load_tail = [&](Ops &o) {
-    const long g = 4 * long(S);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      o.w[t] = *reinterpret_cast<const u32x4m *>(wrow[t] + std::min(g + R, long(G) - 1));
-      o.s[t].x = srow[t][std::min(g + 0, long(G) - 1)];
-      o.s[t].y = srow[t][std::min(g + 1, long(G) - 1)];
-      o.s[t].z = srow[t][std::min(g + 2, long(G) - 1)];
-      o.s[t].w = srow[t][std::min(g + 3, long(G) - 1)];
-    }
-#pragma unroll
-    for (int u = 0; u < MT; ++u)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) load_x(o.x[u][q], u, std::min(g + q, long(G) - 1));
-  };
-
-  float acc[MT][NT][4];
+  float acc[MT][NT][MR];
 #pragma unroll
   for (int u = 0; u < MT; ++u)
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[u][t][r] = 0.0f;
-  const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int r = 0; r < MR; ++r) acc[u][t][r] = 0.0f;
 
-  // one group's products of 16-bit activations
-  auto group16 = [&](const Ops &o, const u32x4m (&w)[NT], int q) {
+  const int blocks = (G + kEsBlock - 1) / kEsBlock;
+  const int mine = it.e >= 0 && blocks > kw ? (blocks - kw + KW - 1) / KW : 0;
+  if (mine > 0) {
+    // The tile's first row of W and its scales (gate; the up rows are N
+    // further), and this lane's row offsets from them (below 2^23 bytes).
+    // Rows past N read row N - 1.
+    const long row = long(it.e) * (kSw ? 2 * long(N) : long(N)) + n0;
+    const char *wbase = reinterpret_cast<const char *>(a.qw) + row * G * 16;
+    const char *sbase = reinterpret_cast<const char *>(a.sc) + row * G * 4;
+    const long up_w = kSw ? long(N) * G * 16 : 0, up_s = kSw ? long(N) * G * 4 : 0;
+    uint32_t woff[NO], soff[NO];
 #pragma unroll
-    for (int u = 0; u < MT; ++u) {
-      if constexpr (!kLimbs) {
-        const u32x4m xa = interleave8(o.x[u][q].v);
+    for (int t = 0; t < NO; ++t) {
+      woff[t] = uint32_t(std::min(n0 + 16 * t + c, N - 1) - n0) * uint32_t(G) * 16u;
+      soff[t] = uint32_t(std::min(n0 + 16 * t + lane / 4, N - 1) - n0) * uint32_t(G) * 4u;
+    }
+    // the activations (slots past the item repeat its last)
+    const int slot = (c >> 2) + 4 * (MT > 1 ? (c & 3) : std::min(c & 3, MR - 1));
+    const char *xrow[MT];
+#pragma unroll
+    for (int u = 0; u < MT; ++u)
+      xrow[u] = static_cast<const char *>(a.X) +
+                2 * (row_of(a, it.row0 + std::min(16 * u + slot, it.rows - 1)) * a.ldx + 8 * R);
+    const long plane = 2 * long(a.rows_x) * a.ldx;
+
+    // step j of block b; groups past G read group G - 1 and are left out later.
+    // Weights and activations are loaded together and equally far ahead: loads
+    // complete in order, so a wait for activations loaded late would be a wait
+    // for every weight asked for before them.
+    struct Ops {
+      u32x4m w[NT];
+      XChunk<XT> x[MT][4];
+    };
+    auto load = [&](Ops &o, int b, int j) {
+      const uint32_t gw = 16u * uint32_t(std::min(b * kEsBlock + 4 * j + R, G - 1));
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        o.w[t] = *reinterpret_cast<const u32x4m *>(wbase + (t < NO ? 0 : up_w) + (woff[t % NO] + gw));
+#pragma unroll
+      for (int u = 0; u < MT; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const long g = 64 * long(std::min(b * kEsBlock + 4 * j + q, G - 1));
+          o.x[u][q].v[0] = *reinterpret_cast<const u32x4m *>(xrow[u] + g);
+          if constexpr (kLimbs)
+            o.x[u][q].v[1] = *reinterpret_cast<const u32x4m *>(xrow[u] + plane + g);
+        }
+    };
+    // Scales of block b: lane l takes 4 groups of row l / 4 of each tile, the
+    // last shares moved back to end at G.
+    auto load_s = [&](f32x4u (&s)[NT], int b) {
+      const uint32_t at = 4u * uint32_t(std::min(b * kEsBlock + 4 * (lane & 3), G - 4));
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        s[t] = *reinterpret_cast<const f32x4u *>(sbase + (t < NO ? 0 : up_s) + (soff[t % NO] + at));
+    };
+    // the same for rows of fewer than 4 groups
+    auto load_few = [&](f32x4u (&s)[NT]) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          s[t][i] = *reinterpret_cast<const float *>(
+              sbase + (t < NO ? 0 : up_s) + (soff[t % NO] + 4u * uint32_t(std::min(i, G - 1))));
+    };
+    // Into the wave's words, group q of row n of the block at 16 n + q: a whole
+    // block, or the last one, whose moved shares write their groups' own places.
+    float *keep = mem + 16 * (lane / 4);
+    auto keep_s = [&](const f32x4u (&s)[NT]) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        *reinterpret_cast<float4 *>(keep + 256 * t + 4 * (lane & 3)) =
+            make_float4(s[t][0], s[t][1], s[t][2], s[t][3]);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+    auto keep_last = [&](const f32x4u (&s)[NT], int b) {
+      const int g = 4 * (lane & 3);
+      const int moved = G >= 4 ? std::max(b * kEsBlock + g - (G - 4), 0) : 0;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i >= moved) keep[256 * t + g + i - moved] = s[t][i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+
+    const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto group = [&](const Ops &o, const float4 (&sc)[NT], int q) {
+#pragma unroll
+      for (int u = 0; u < MT; ++u) {
+        const u32x4m xa = kLimbs ? o.x[u][q].v[0] : interleave8(o.x[u][q].v[0]);
         floatx4 d0 = zero;
-        if constexpr (sizeof(XT) == 2 && !__is_same(XT, _Float16)) {
+        if constexpr (__is_same(XT, Bf16)) {
           const bf16x8 off = __builtin_bit_cast(
               bf16x8, u32x4m{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u});  // -24
           d0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xa), off, zero, 0,
@@ -203,197 +231,173 @@ __global__ void __launch_bounds__(kEsThreads) experts_skinny(ExpertArgs a) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           floatx4 d;
-          if constexpr (__is_same(XT, _Float16))
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, xa),
-                                                       nibbles_to_f16(w[t][q]), zero, 0, 0, 0);
-          else
+          if constexpr (__is_same(XT, Bf16)) {
             d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xa),
-                                                        nibbles_to_bf16_16(w[t][q]), d0, 0, 0, 0);
-          const float s4[4] = {o.s[t].x, o.s[t].y, o.s[t].z, o.s[t].w};
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[u][t][r] = fmaf(s4[q], d[r], acc[u][t][r]);
-        }
-      }
-    }
-  };
-  // a pair of groups' products of fp32 activations (two: the pair is whole)
-  float *inv = es_inv + wave * 16 * MT;
-  auto pair32 = [&](const Ops &o, const u32x4m (&w)[NT], int q0, bool two) {
-    if constexpr (kLimbs) {
-      float up[MT];
-#pragma unroll
-      for (int u = 0; u < MT; ++u) {
-        // the slot's largest magnitude in the pair: this lane's 16 values,
-        // then the slot's 4 lanes
-        const float4 a0 = o.x[u][q0].lo, a1 = o.x[u][q0].hi;
-        const float4 a2 = o.x[u][q0 + 1].lo, a3 = o.x[u][q0 + 1].hi;
-        const float t0 = limb_absmax3(a0.x, a0.y, a0.z), t1 = limb_absmax3(a0.w, a1.x, a1.y);
-        const float t2 = limb_absmax3(a1.z, a1.w, a2.x), t3 = limb_absmax3(a2.y, a2.z, a2.w);
-        const float t4 = limb_absmax3(a3.x, a3.y, a3.z), t5 = limb_absmax3(t0, t1, a3.w);
-        float mx = limb_absmax3(t2, t3, t4);
-        mx = limb_absmax3(mx, t5, 0.0f);
-        const auto h32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx),
-                                                          false, false);
-        mx = limb_absmax3(__uint_as_float(h32[0]), __uint_as_float(h32[1]), 0.0f);
-        const auto h16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(mx), __float_as_uint(mx),
-                                                          false, false);
-        mx = limb_absmax3(__uint_as_float(h16[0]), __uint_as_float(h16[1]), 0.0f);
-        // e in [-113, 116]: 2^-e and 2^(e+11) are normal, x 2^(e+11) finite
-        const int e = std::min(row_exponent(mx), 116);
-        if (R == 0) inv[16 * u + c] = __int_as_float((127 - e) << 23);
-        up[u] = __int_as_float((127 + e + 11) << 23);
-      }
-      // this wave's own words (its LDS operations complete in order)
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      float4 fac[MT];
-#pragma unroll
-      for (int u = 0; u < MT; ++u)
-        fac[u] = *reinterpret_cast<const float4 *>(inv + 16 * u + 4 * R);
-      float ss[MT][NT][4];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (q == 1 && !two) break;
-        half8_t hi[MT], lo[MT];
-#pragma unroll
-        for (int u = 0; u < MT; ++u) {
-          const float4 x0 = o.x[u][q0 + q].lo, x1 = o.x[u][q0 + q].hi;
-          const float va[4] = {x0.x, x0.y, x0.z, x0.w}, vb[4] = {x1.x, x1.y, x1.z, x1.w};
-          uint32_t hw[4], lw[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            limb_split2(va[i] * up[u], vb[i] * up[u], 0x1p-11f, -2048.0f, hw[i], lw[i]);
-          hi[u] = __builtin_bit_cast(half8_t, make_uint4(hw[0], hw[1], hw[2], hw[3]));
-          lo[u] = __builtin_bit_cast(half8_t, make_uint4(lw[0], lw[1], lw[2], lw[3]));
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const half8_t b = nibbles_to_f16(w[t][q0 + q]);
-          const _Float16 k2 = (_Float16)0x1p-11f;
-          const half8_t b2 = b * half8_t{k2, k2, k2, k2, k2, k2, k2, k2};  // exact in fp16
-          const float s4[4] = {o.s[t].x, o.s[t].y, o.s[t].z, o.s[t].w};
-          const float sq = s4[q0 + q];
-#pragma unroll
-          for (int u = 0; u < MT; ++u) {
-            floatx4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi[u], b, zero, 0, 0, 0);
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo[u], b2, d, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              ss[u][t][r] = q == 0 ? sq * d[r] : fmaf(sq, d[r], ss[u][t][r]);
+                                                        nibbles_to_bf16_16(o.w[t][q]), d0, 0, 0, 0);
+          } else {
+            const half8_t b = nibbles_to_f16(o.w[t][q]);
+            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, xa), b, zero, 0,
+                                                       0, 0);
+            if constexpr (kLimbs)
+              d = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                  __builtin_bit_cast(half8_t, o.x[u][q].v[sizeof(XT) / 4]), b, d, 0, 0, 0);
           }
+          const float s = q == 0 ? sc[t].x : q == 1 ? sc[t].y : q == 2 ? sc[t].z : sc[t].w;
+#pragma unroll
+          for (int r = 0; r < MR; ++r) acc[u][t][r] = fmaf(s, d[r], acc[u][t][r]);
         }
       }
+    };
+    // left: groups of the step that there are
+    auto process = [&](Ops &o, int j, int left) {
+      float4 sc[NT];
 #pragma unroll
-      for (int u = 0; u < MT; ++u) {
-        const float f[4] = {fac[u].x, fac[u].y, fac[u].z, fac[u].w};
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[u][t][r] = fmaf(ss[u][t][r], f[r], acc[u][t][r]);
+      for (int t = 0; t < NT; ++t) {
+        sc[t] = *reinterpret_cast<const float4 *>(mem + 16 * (16 * t + c) + 4 * j);
+        transpose_words(o.w[t]);
       }
-    }
-  };
-  // left: groups of the step (4, or fewer in the last one)
-  auto process = [&](const Ops &o, int left) {
-    u32x4m w[NT];
+      // one group at a time: letting the scheduler mix them costs registers
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      w[t] = o.w[t];
-      transpose_words(w[t]);
-    }
-    if constexpr (kLimbs) {
-      pair32(o, w, 0, left > 1);
-      if (left > 2) pair32(o, w, 2, left > 3);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q < left) group16(o, w, q);
-    }
-  };
+      for (int q = 0; q < 4; ++q) {
+        if (q < left) group(o, sc, q);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
 
-  // wave w takes steps w, w + 8, ...; a ring of P steps in registers
-  Ops ring[P];
+    // A ring of P steps: a step's registers are refilled after their last use,
+    // which keeps them over the loop's back edge.
+    Ops ring[P];
+    f32x4u s[NT];
+    if (G >= 4)
+      load_s(s, kw);
+    else
+      load_few(s);
 #pragma unroll
-  for (int p = 0; p < P; ++p)
-    if (wave + p * kEsWaves < S) load(ring[p], wave + p * kEsWaves);
-  for (int s = wave; s < S; s += P * kEsWaves) {
+    for (int j = 0; j < P; ++j) load(ring[j], kw, j);
+    int b = kw;
+    for (int i = 1; i < mine; ++i) {  // every block but a wave's last is whole
+      keep_s(s);
+      load_s(s, b + KW);
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int at = s + p * kEsWaves;
-      if (at >= S) break;
-      process(ring[p], 4);
-      // refilled after its last use: the ring keeps its registers over the
-      // loop's back edge, and a step waits for its own loads only
-      __builtin_amdgcn_sched_barrier(0);
-      if (at + P * kEsWaves < S) load(ring[p], at + P * kEsWaves);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < 4; ++j) {
+        process(ring[j % P], j, 4);
+        load(ring[j % P], j + P < 4 ? b : b + KW, (j + P) % 4);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      b += KW;
+    }
+    keep_last(s, b);
+    const int rest = G - b * kEsBlock;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (4 * j >= rest) break;
+      process(ring[j % P], j, rest - 4 * j);
+      if (j + P < 4) load(ring[j % P], b, j + P);
     }
   }
-  // the last G % 4 groups, on the wave whose turn it would be
-  if (G % 4 != 0 && wave == S % kEsWaves) {
-    Ops o;
-    load_tail(o);
-    process(o, G % 4);
-  }
 
+  if constexpr (KW > 1) {
+    // sums of the tile's waves, in their order, on the first of them (each wave
+    // is past its own words)
+#pragma unroll
+    for (int u = 0; u < MT; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < MR; ++r) mem[((u * NT + t) * MR + r) * 64 + lane] = acc[u][t][r];
+    __syncthreads();
+    if (kw != 0) return;
+#pragma unroll
+    for (int u = 0; u < MT; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < MR; ++r)
+#pragma unroll
+          for (int k = 1; k < KW; ++k)
+            acc[u][t][r] += mem[k * kWaveLds + ((u * NT + t) * MR + r) * 64 + lane];
+  }
+  if (it.e < 0) return;
 #pragma unroll
   for (int u = 0; u < MT; ++u)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int r = 0; r < MR; ++r) {
+      const int m = 16 * u + R + 4 * r;
+      if (m >= it.rows) continue;
+      float f = 1.0f;
+      if constexpr (kLimbs) f = a.factor[row_of(a, it.row0 + m)];
+      const long y = long(it.row0 + m) * a.ldy;
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        red[wave * kTile + ((u * NT + t) * 4 + r) * 64 + lane] = acc[u][t][r];
-  __syncthreads();
-  for (int i = threadIdx.x; i < MT * NO * 256; i += kEsThreads) {
-    const int l = i & 63, r = (i >> 6) & 3, ut = i >> 8;
-    const int u = ut / NO, t = ut - u * NO;
-    const int at = ((u * NT + t) * 4 + r) * 64 + l;
-    const int m = 16 * u + 4 * (l >> 4) + r, n = n0 + 16 * t + (l & 15);
-    if (m >= it.rows || n >= N) continue;
-    float g = 0.0f, v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kEsWaves; ++w) {
-      g += red[w * kTile + at];
-      if constexpr (kSw) v += red[w * kTile + at + NO * 256];
+      for (int t = 0; t < NO; ++t) {
+        const int n = n0 + 16 * t + c;
+        if (n >= N) continue;
+        const float g = acc[u][t][r] * f;
+        if constexpr (kSw)
+          static_cast<XT *>(a.Y)[y + n] = from_f32<XT>(silu_mul(g, acc[u][t + NO][r] * f));
+        else
+          static_cast<float *>(a.Y)[y + n] = g;
+      }
     }
-    const long y = long(it.row0 + m) * a.ldy + n;
-    if constexpr (kSw)
-      static_cast<XT *>(a.Y)[y] = from_f32<XT>(silu_mul(g, v));
-    else
-      static_cast<float *>(a.Y)[y] = g;
-  }
 }
 
-template <typename XT, int MT, int NT, int P, bool kSw>
+template <typename XT, int MT, int MR, int NT, int KW, int P, int kOcc, bool kSw>
 hipError_t run_skinny(ExpertArgs a, hipStream_t stream) {
   constexpr int NO = kSw ? NT / 2 : NT;
+  constexpr int B = MT > 1 ? 16 * MT : 4 * MR;
   a.tiles_n = (a.N + 16 * NO - 1) / (16 * NO);
-  const long blocks = long(a.tiles_n) * max_items(a.R, a.E, 16 * MT);
+  const long tiles = long(a.tiles_n) * max_items(a.R, a.E, B);
+  const long blocks = (tiles * KW + kEsWaves - 1) / kEsWaves;
   if (blocks < 1 || blocks > 0x7fffffffL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((experts_skinny<XT, MT, NT, P, kSw>), dim3(unsigned(blocks)),
+  hipLaunchKernelGGL((experts_skinny<XT, MT, MR, NT, KW, P, kOcc, kSw>), dim3(unsigned(blocks)),
                      dim3(kEsThreads), 0, stream, a);
   return hipGetLastError();
 }
 
+template <typename XT, bool kSw, int KW>
+hipError_t run_skinny_rows(const ExpertArgs &a, hipStream_t stream) {
+  constexpr bool kLimbs = sizeof(XT) == 4;
+  switch (experts_skinny_rows(a.R, a.E)) {
+    case 4: return run_skinny<XT, 1, 1, 4, KW, 2, 2, kSw>(a, stream);
+    case 8: return run_skinny<XT, 1, 2, 4, KW, 2, 2, kSw>(a, stream);
+    case 16: return run_skinny<XT, 1, 4, 4, KW, 2, 2, kSw>(a, stream);
+    case 32: return run_skinny<XT, 2, 4, 2, KW, kLimbs ? 1 : 2, 2, kSw>(a, stream);
+    default: return run_skinny<XT, 4, 4, 2, KW, 1, 2, kSw>(a, stream);
+  }
+}
+
 template <typename XT, bool kSw>
 hipError_t run_skinny_type(const ExpertArgs &a, hipStream_t stream) {
-  switch (experts_skinny_rows(a.R, a.E)) {
-    case 16: return run_skinny<XT, 1, 4, 2, kSw>(a, stream);
-    case 32: return run_skinny<XT, 2, 4, 2, kSw>(a, stream);
-    default: return run_skinny<XT, 4, 2, sizeof(XT) == 4 ? 1 : 2, kSw>(a, stream);
-  }
+  // Waves per tile: as many as there are blocks for up to 2, where few tiles
+  // leave the card to fill up to 4 (K = 7168, one token, 32 tiles: 15.8 against
+  // 24.5 us with 2; 512 tiles: 37.2 against 35.2).
+  const int blocks = (a.G + kEsBlock - 1) / kEsBlock;
+  const long tiles = (long(a.N) + 31) / 32 * std::min(a.R, a.E);
+  if (blocks >= 4 && tiles < 512) return run_skinny_rows<XT, kSw, 4>(a, stream);
+  if (blocks >= 2) return run_skinny_rows<XT, kSw, 2>(a, stream);
+  return run_skinny_rows<XT, kSw, 1>(a, stream);
 }
 
 }  // namespace
 
-// slots per workgroup: enough for one block of most experts
+// slots per item: enough for one item of most experts
 int experts_skinny_rows(long R, long E) {
   const double mean = double(R) / double(std::max(1L, std::min(R, E)));
-  return mean <= 10.0 ? 16 : mean <= 24.0 ? 32 : 64;
+  return mean <= 1.25 ? 4 : mean <= 4.0 ? 8 : mean <= 10.0 ? 16 : mean <= 24.0 ? 32 : 64;
 }
 
 hipError_t launch_experts_skinny(const MoeExperts &p, hipStream_t stream) {
   ExpertArgs a;
   a.X = p.X;
+  a.ldx = p.K;
+  a.factor = nullptr;
+  if (p.dtype == W4A16_DTYPE_F32) {
+    const LimbLayout at = limb_layout(p.workspace, p.rows_x, p.K, p.dtype);
+    const hipError_t e = launch_limbs(p, stream);
+    if (e != hipSuccess) return e;
+    a.X = at.limbs;
+    a.factor = at.factor;
+    a.ldx = at.KP;
+  }
   a.token_index = p.token_index;
   a.offsets = p.expert_offsets;
   a.qw = reinterpret_cast<const uint4 *>(p.qweight);

@@ -1,13 +1,9 @@
 // Experts' W4A16 products for many slots per expert (prompts): the products of
 // moe_skinny.hip in 128 x 128 tiles on the fp16 matrix instructions.
 //
-// A first kernel turns the activations into fp16 limbs in the workspace, once
-// for all the tiles that read them: a row is scaled by a power of two (its
-// largest magnitude into [2^14, 2^15); fp16 rows stay as they are), and kept
-// as one limb (fp16, bf16: exact for every value within 2^-28 of its row's
-// largest) or two (fp32: 22 significant bits down to 2^-17 of the row's
-// largest, below that an absolute error under 2^-39 of it).  Each 8 values
-// are stored in the order of the nibble conversion.
+// The activations come as fp16 limbs that moe_limbs.hip makes in the workspace,
+// once for all the tiles that read them: one limb for fp16 and bf16, two for
+// fp32.
 //
 // The tile kernel: v_mfma_f32_16x16x32_f16 on limbs and the exact codes q - 8
 // (K: one group of 32; every product exact in fp32), one fp32 FMA per output
@@ -62,77 +58,6 @@ __device__ __forceinline__ void et_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
-
-// ------------------------------------------------------------------ limbs
-//
-// Workspace: limb plane l of row t at (l * rows + t) * KP fp16 values, KP = K
-// rounded up to 64 (zeros behind K), then one fp32 factor 2^-e per row.
-
-__device__ __forceinline__ void read8(const float *p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void read8(const _Float16 *p, float (&v)[8]) {
-  const half8_t a = *reinterpret_cast<const half8_t *>(p);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = float(a[i]);
-}
-__device__ __forceinline__ void read8(const Bf16 *p, float (&v)[8]) {
-  const u32x4m a = *reinterpret_cast<const u32x4m *>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(a[i] << 16);
-    v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-  }
-}
-
-constexpr int kPrepThreads = 256;
-
-// One row per workgroup.
-template <typename XT>
-__global__ void __launch_bounds__(kPrepThreads)
-experts_limbs(const XT *__restrict__ X, _Float16 *__restrict__ limbs, float *__restrict__ factor,
-              int rows, int K, int KP) {
-  __shared__ float part[kPrepThreads / 64];
-  const long t = blockIdx.x;
-  const int tid = threadIdx.x;
-  const XT *x = X + t * K;
-  int e = 0;
-  if constexpr (!__is_same(XT, _Float16)) {
-    float mx = 0.0f;
-    for (int k = 8 * tid; k < K; k += 8 * kPrepThreads) {
-      float v[8];
-      read8(x + k, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]));
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
-    if ((tid & 63) == 0) part[tid >> 6] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-    e = std::min(row_exponent(mx), 126);  // 2^-e is a normal number
-  }
-  if (tid == 0) factor[t] = ldexpf(1.0f, -e);
-  _Float16 *hi = limbs + t * KP, *lo = hi + long(rows) * KP;
-  for (int k = 8 * tid; k < KP; k += 8 * kPrepThreads) {
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (k < K) read8(x + k, v);
-    half8_t h, l;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int j = (i >> 1) + 4 * (i & 1);  // x0 x4 x1 x5 x2 x6 x3 x7
-      const float s = ldexpf(v[j], e);
-      h[i] = _Float16(s);
-      l[i] = _Float16(s - float(h[i]));
-    }
-    *reinterpret_cast<half8_t *>(hi + k) = h;
-    if constexpr (sizeof(XT) == 4) *reinterpret_cast<half8_t *>(lo + k) = l;
-  }
-}
-
-// ------------------------------------------------------------------ tiles
 
 struct TileArgs {
   const _Float16 *limbs;
@@ -341,12 +266,11 @@ template <typename XT, bool kSw>
 hipError_t run_tile(const MoeExperts &p, hipStream_t stream) {
   using OT = typename std::conditional<kSw, XT, float>::type;
   constexpr int L = sizeof(XT) == 4 ? 2 : 1;
+  const LimbLayout at = limb_layout(p.workspace, p.rows_x, p.K, p.dtype);
   TileArgs a;
-  a.KP = (p.K + 63) / 64 * 64;
-  _Float16 *limbs = static_cast<_Float16 *>(p.workspace);
-  float *factor = reinterpret_cast<float *>(limbs + size_t(L) * p.rows_x * a.KP);
-  a.limbs = limbs;
-  a.factor = factor;
+  a.KP = at.KP;
+  a.limbs = at.limbs;
+  a.factor = at.factor;
   a.token_index = p.token_index;
   a.offsets = p.expert_offsets;
   a.qw = reinterpret_cast<const unsigned char *>(p.qweight);
@@ -361,9 +285,7 @@ hipError_t run_tile(const MoeExperts &p, hipStream_t stream) {
   a.tiles_n = (p.N + (kSw ? 64 : 128) - 1) / (kSw ? 64 : 128);
   const long tiles = long(a.tiles_n) * max_items(p.R, p.E, 128);
   if (tiles < 1 || tiles > 0x7ffffff0L) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(experts_limbs<XT>, dim3(unsigned(p.rows_x)), dim3(kPrepThreads), 0, stream,
-                     static_cast<const XT *>(p.X), limbs, factor, p.rows_x, p.K, a.KP);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = launch_limbs(p, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((experts_tile<L, OT, kSw>), dim3(unsigned((tiles + 7) / 8 * 8)),
                      dim3(kEtThreads), 0, stream, a);
@@ -383,10 +305,9 @@ int experts_kernel(long R, long E) {
 }
 
 size_t experts_workspace_bytes(long rows_x, long R, long E, int K, int dtype) {
-  if (experts_kernel(R, E) != W4A16_EXPERTS_TILE) return 0;
-  const size_t KP = size_t(K + 63) / 64 * 64;
-  return (size_t(rows_x) * KP * (dtype == W4A16_DTYPE_F32 ? 4 : 2) + size_t(rows_x) * 4 + 255) /
-         256 * 256;
+  // the skinny kernel takes 16-bit activations as they are
+  if (experts_kernel(R, E) != W4A16_EXPERTS_TILE && dtype != W4A16_DTYPE_F32) return 0;
+  return limb_bytes(rows_x, K, dtype);
 }
 
 hipError_t launch_experts_tile(const MoeExperts &p, hipStream_t stream) {

@@ -162,7 +162,17 @@ struct MoeExperts {
   int rows_x, R, E, N, K, ldy, dtype;
   bool swiglu;
 };
-// W4A16_EXPERTS_*: the kernel for a shape; its workspace (0 for the skinny one)
+// fp16 limbs of the activations in the workspace (moe_limbs.hip): 2 planes for
+// fp32, 1 for the 16-bit types, rows of KP values, then a factor per row
+struct LimbLayout {
+  _Float16 *limbs;
+  float *factor;
+  int KP;
+};
+LimbLayout limb_layout(void *workspace, long rows, int K, int dtype);
+size_t limb_bytes(long rows, int K, int dtype);
+hipError_t launch_limbs(const MoeExperts &p, hipStream_t stream);
+// W4A16_EXPERTS_*: the kernel for a shape; its workspace
 int experts_kernel(long R, long E);
 size_t experts_workspace_bytes(long rows_x, long R, long E, int K, int dtype);
 hipError_t launch_experts(const MoeExperts &p, hipStream_t stream);

@@ -35,7 +35,8 @@ def route(logits, topk, bias=None, score="softmax", groups=1, group_limit=1, gro
                 p = np.where(x == x.max(), 1.0, np.exp(x - x.max()))
                 s = np.where(open_, p, 0.0) / p[open_].sum()
             key = x.copy() if bias is None else s + np.asarray(bias, dtype=np.float64)
-            worth = s if bias is None else key  # what groups are valued by
+            # what groups are valued by
+            worth = s if bias is None and group_top == 2 else key
         masked = ~open_ | np.isnan(key) | (key == -np.inf)
         if group_limit < groups:
             size = E // groups
