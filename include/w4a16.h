@@ -567,7 +567,8 @@ size_t w4a16_grouped_swiglu_workspace_bytes(int64_t T, int64_t R, int64_t E, int
  * meet it with scale * |x| * (q + 40) in place of |x * w| (the skinny kernel
  * multiplies by q + 16 and takes 24 off again in fp32); the tile kernel scales
  * them per row into fp16, exactly for values down to 2^-28 of their row's
- * largest.  A row of X holding Inf or NaN gives non-finite values in its slots.
+ * largest, and takes the scales and weights in fp16's 11 bits (at most 2^-10 of
+ * |x * w| more).  A row of X holding Inf or NaN gives non-finite values in its slots.
  * workspace: w4a16_grouped_swiglu_workspace_bytes, 256-byte aligned; may be
  * NULL where that is 0.  R == 0 or F == 0 is a no-op; T == 0 with R > 0 is
  * W4A16_ERR_ARG; an unknown dtype is W4A16_ERR_ARG; X and qweight 16-byte

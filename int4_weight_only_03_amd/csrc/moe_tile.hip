@@ -5,32 +5,39 @@
 // once for all the tiles that read them: one limb for fp16 and bf16, two for
 // fp32.
 //
-// The tile kernel: v_mfma_f32_16x16x32_f16 on limbs and the exact codes q - 8
-// (K: one group of 32; every product exact in fp32), one fp32 FMA per output
-// and group for the scale, the row's power of two undone at the store.  A
-// workgroup takes 128 slots of one expert by 128 rows of W (gate/up form: 64
-// gate rows and the up rows of the same outputs, so that both sums of an
-// output lie in one lane); wave (wm, wn) of its 4 waves 64 x 64 of them.
+// The tile kernel: v_mfma_f32_16x16x32_f16 (K: one group of 32), fp32
+// accumulation, the row's power of two undone at the store.  A workgroup takes
+// 16 U slots (U = 8, 4 or 2, by the mean number of an expert) of one expert by
+// 256 rows of W (gate/up form: 128 gate rows and the up rows of the same
+// outputs, so that both sums of an output lie in one lane); each of its 4 waves
+// all of the slots by 64 of the rows, so that no weight is converted twice.
+// The weights:
+//   fp32, fp16  the exact codes q - 8, every product exact in fp32, one fp32
+//         FMA per output and group for the scale;
+//   bf16  (q - 8) * scale * 2^10 in fp16, the scale rounded to it and the
+//         product, so that the products of all groups add up inside the matrix
+//         instructions.  Those roundings, at most 2^-10 of a weight together and
+//         independent from group to group, move a sum by about 2^-12 of its
+//         size beside the 2^-8 that the stored result is rounded by (fp16's
+//         2^-11 leaves no such room), and save the FMAs, 256 VALU instructions
+//         of a wave's 400 per stage.  A scale outside [2^-20, 4) would leave
+//         fp16's range: its group counts as 0 there, and a stage with such a
+//         group adds its exact codes' products, scaled in fp32, by themselves.
 //
-// Per stage of two groups: the limbs come to LDS by direct copies (gathered
-// rows, 128 bytes each), the weight words through registers, converted once
-// per workgroup into an LDS image of codes; both images are double buffered
-// and a stage has one barrier.  While a stage's products run, the next stage's
-// copies fly and its codes are converted.
+// Stages of two groups.  Limbs (gathered rows, 128 bytes each), weight words and
+// scales come to LDS by direct copies, two stages ahead, into three images; a
+// stage has one barrier.  A wave copies the weights and scales of its own rows.
 //
 // Tiles are dealt so that each XCD works a contiguous run of them (the
 // hardware deals workgroups round-robin over the 8 XCDs), row blocks of an
 // expert fastest: the tiles an XCD holds at once share weight rows and slots.
-//
-// Bound: VALU issue.  Per stage and wave 32 L matrix instructions (16 cycles
-// each; L limbs) against 128 FMAs for the scales, 36 for the conversion and
-// about 30 others of 4 cycles.
 
 #include "moe_common.h"
 #include "gemv_common.h"
 #include "limbs.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace w4a16 {
 namespace {
@@ -39,8 +46,10 @@ typedef __attribute__((address_space(3))) void et_lds_void;
 
 constexpr int kEtThreads = 256;
 
-__device__ __forceinline__ void et_wait_vm0() {
-  __builtin_amdgcn_s_waitcnt(0x70 | (15 << 8));  // vmcnt(0)
+template <int VM>
+__device__ __forceinline__ void et_wait_vm() {  // at most VM copies still in flight
+  static_assert(VM >= 0 && VM < 64, "wait count");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70 | (15 << 8));
 }
 __device__ __forceinline__ void et_wait_lgkm0() {
   __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | 0x70);  // lgkmcnt(0)
@@ -53,10 +62,23 @@ __device__ __forceinline__ void et_copy16(const void *src, const void *lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 1\n\tglobal_load_lds_dwordx4 %0, off"
                :: "v"(src), "s"(at) : "memory", "m0");
 }
+__device__ __forceinline__ void et_copy4(const void *src, const void *lds) {
+  const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>((const et_lds_void *)lds));
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 1\n\tglobal_load_lds_dword %0, off"
+               :: "v"(src), "s"(at) : "memory", "m0");
+}
 __device__ __forceinline__ void et_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+constexpr float kFold = 1024.0f;  // power of two of folded weights
+
+// whether a scale times kFold is folded in (0 is: its products are 0 either way)
+__device__ __forceinline__ bool foldable(float s) {
+  const float m = fabsf(s);
+  return bool(int(m == 0.0f) | (int(m >= 0x1p-10f) & int(m < 4096.0f)));
 }
 
 struct TileArgs {
@@ -69,50 +91,52 @@ struct TileArgs {
   int rows_x, R, E, N, G, KP, ldy, tiles_n;
 };
 
-// L limbs, OT the output type (kSw: the activations' type, else fp32)
-template <int L, typename OT, bool kSw>
-__global__ void __launch_bounds__(kEtThreads, L == 1 ? 2 : 1) experts_tile(TileArgs a) {
-  // Images of a stage (64 k): row r at 128 r, logical chunk x (16 bytes: 8
-  // values of one group's block x % 4, group x / 4) at chunk x ^ ((r / 2) % 8),
-  // so that the 16 rows an operand read touches fall in distinct banks.
-  __shared__ __align__(16) unsigned char et_a0[L * 16384];
-  __shared__ __align__(16) unsigned char et_a1[L * 16384];
-  __shared__ __align__(16) unsigned char et_c0[16384];
-  __shared__ __align__(16) unsigned char et_c1[16384];
-  __shared__ __align__(16) float et_s0[256];  // scales: row n, group q at 2 n + q
-  __shared__ __align__(16) float et_s1[256];
-  constexpr int NO = kSw ? 64 : 128;  // outputs per tile
+// U: row tiles of 16 slots, L limbs, OT the output type (kSw: the activations'
+// type, else fp32), kFolded: weights with their scales.
+template <int U, int L, typename OT, bool kSw, bool kFolded>
+__global__ void __launch_bounds__(kEtThreads, U == 8 && L == 2 ? 1 : 2) experts_tile(TileArgs a) {
+  static_assert(!kFolded || L == 1, "folded weights have fp16's precision");
+  // An image of a stage (64 k).
+  // Limbs: row r at 128 r, logical chunk x (16 bytes: 8 values of one group's
+  // block x % 4, group x / 4) at chunk x ^ ((r / 2) % 8), so that the 16 rows an
+  // operand read touches fall in distinct banks.
+  // Weights: W row n at 32 n, its 16 bytes of group q at half q ^ ((n / 8) % 2),
+  // for the same reason.  Scales: group q of row n at 8 n + 4 q.
+  constexpr int kRows = 16 * U, kLimb = kRows * 128;
+  constexpr int kW = L * kLimb, kS = kW + 8192, kImage = kS + 2048;
+  __shared__ __align__(16) unsigned char et_mem[3 * kImage];
+  constexpr int kCopies = L * (U / 2) + 4;  // of a wave and stage
+  constexpr int NO = kSw ? 128 : 256;       // outputs per tile
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
   const int c = lane & 15, R = lane >> 4;
   const int G = a.G, N = a.N;
 
   // tile of this workgroup: XCD b % 8 takes a contiguous run of the tiles
   // there are; within an expert its row blocks are fastest
-  ExpertItem it = find_item(a.offsets, a.E, a.R, 128, 0);
+  ExpertItem it = find_item(a.offsets, a.E, a.R, kRows, 0);
   const long tiles = long(it.total) * a.tiles_n;
   const long run = (tiles + 7) / 8;
   const long index = long(blockIdx.x >> 3);
   const long tile = long(blockIdx.x & 7) * run + index;
   if (index >= run || tile >= tiles) return;  // uniform over the workgroup
-  it = find_item(a.offsets, a.E, a.R, 128, int(tile / a.tiles_n));
+  it = find_item(a.offsets, a.E, a.R, kRows, int(tile / a.tiles_n));
   // tiles of this expert: it.blocks x tiles_n, from item (its first block) on
   const long first = (tile / a.tiles_n - it.block) * a.tiles_n;
   const int within = int(tile - first);
   const int bm = within % it.blocks, bn = within / it.blocks;
   int e0, e1;
   expert_slots(a.offsets, it.e, a.R, e0, e1);
-  const int row0 = e0 + bm * 128, rows = std::min(128, e1 - row0);
+  const int row0 = e0 + bm * kRows, rows = std::min(kRows, e1 - row0);
   const int n0 = bn * NO;
 
-  // Limb copies: copy j (wave w issues j = 4w .. 4w+3 of each limb): lane i
-  // writes 16 B at 1024 j + 16 i: row 8 j + i / 8, chunk i % 8, which holds
-  // logical chunk (i % 8) ^ ((row / 2) % 8).  Rows past the item repeat its last.
-  const unsigned char *asrc[4];
+  // Limb copies: copy j (wave w issues j = w U/2 .. of each limb): lane i writes
+  // 16 B at 1024 j + 16 i: row 8 j + i / 8, chunk i % 8, which holds logical
+  // chunk (i % 8) ^ ((row / 2) % 8).  Rows past the item repeat its last.
+  const unsigned char *asrc[U / 2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = 8 * (4 * wave + j) + lane / 8;
+  for (int j = 0; j < U / 2; ++j) {
+    const int r = 8 * (wave * (U / 2) + j) + lane / 8;
     const int slot = row0 + std::min(r, rows - 1);
     long row = slot;
     if (a.token_index) row = std::min(std::max(a.token_index[slot], 0), a.rows_x - 1);
@@ -120,149 +144,200 @@ __global__ void __launch_bounds__(kEtThreads, L == 1 ? 2 : 1) experts_tile(TileA
               16 * ((lane & 7) ^ ((r >> 1) & 7));
   }
   const long plane = long(a.rows_x) * a.KP * 2;
+  // Row of W of row i of this wave's 64.  Gate/up form: 0..31 are gate rows of
+  // outputs n0 + 32 w .. +31, 32..63 the up rows of the same.  Rows past N read
+  // row N - 1.
+  auto w_row = [&](int i) -> long {
+    long n;
+    if constexpr (kSw)
+      n = std::min(n0 + 32 * wave + (i & 31), N - 1) + ((i & 32) ? long(N) : 0);
+    else
+      n = std::min(n0 + 64 * wave + i, N - 1);
+    return n + long(it.e) * (kSw ? 2 * long(N) : long(N));
+  };
+  // Weight copies j = 0, 1: lane i writes 16 B: row 32 j + i / 2, half i % 2.
+  // Scale copies: lane i writes 4 B: row 32 j + i / 2, group i % 2.
+  const unsigned char *wsrc[2];
+  const float *ssrc[2];
+  int wq[2];  // the lane's group of the stage
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = 32 * j + lane / 2;
+    wq[j] = (lane & 1) ^ ((i >> 3) & 1);
+    wsrc[j] = a.qw + w_row(i) * G * 16 + 16 * wq[j];
+    ssrc[j] = a.sc + w_row(i) * G + (lane & 1);
+  }
+  const int P = (G + 1) / 2;
+  // stage p into an image; called for the stages in order
   auto copy_stage = [&](unsigned char *img, int p) {
+    // an odd G's last stage has one group: the other half reads it again (its
+    // limbs are 0)
+    if (2 * p + 1 >= G) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        wsrc[j] -= wq[j] ? 16 : 0;
+        ssrc[j] -= lane & 1;
+      }
+    }
 #pragma unroll
     for (int l = 0; l < L; ++l)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        et_copy16(asrc[j] + l * plane + long(p) * 128, img + 16384 * l + 1024 * (4 * wave + j));
-  };
-  // Weights: thread t takes image row t / 2, group t % 2 of each stage.  Gate/up
-  // form: image rows 64 wn + 0..31 are gate rows of outputs 32 wn .. +31, rows
-  // 64 wn + 32..63 the up rows of the same.  Rows past N read row N - 1.
-  const int cr = tid >> 1, ch = tid & 1;
-  long wrow;
-  if constexpr (kSw)
-    wrow = std::min(n0 + 32 * (cr >> 6) + (cr & 31), N - 1) + ((cr & 32) ? long(N) : 0);
-  else
-    wrow = std::min(n0 + cr, N - 1);
-  wrow += long(it.e) * (kSw ? 2 * long(N) : long(N));
-  const unsigned char *wsrc = a.qw + wrow * G * 16;
-  const float *ssrc = a.sc + wrow * G;
-  const int P = (G + 1) / 2;
-  struct W {
-    u32x4m w;
-    float s;
-  };
-  auto load_w = [&](int p) -> W {
-    const int g = 2 * p + ch, gc = std::min(g, G - 1);
-    W v;
-    v.w = *reinterpret_cast<const u32x4m *>(wsrc + long(gc) * 16);
-    v.s = g < G ? ssrc[gc] : 0.0f;  // behind the last group the limbs are 0 too
-    return v;
-  };
-  uint32_t cwrite[4];
+      for (int j = 0; j < U / 2; ++j)
+        et_copy16(asrc[j] + l * plane, img + l * kLimb + 1024 * (wave * (U / 2) + j));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) cwrite[i] = uint32_t(cr * 128 + 16 * ((4 * ch + i) ^ ((cr >> 1) & 7)));
-  auto convert = [&](const W &v, unsigned char *cimg, float *simg) {
+    for (int j = 0; j < 2; ++j) {
+      et_copy16(wsrc[j], img + kW + 2048 * wave + 1024 * j);
+      et_copy4(ssrc[j], img + kS + 512 * wave + 256 * j);
+      wsrc[j] += 32;
+      ssrc[j] += 2;
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<half8_t *>(cimg + cwrite[i]) = nibbles_to_f16(v.w[i]);
-    simg[tid] = v.s;
+    for (int j = 0; j < U / 2; ++j) asrc[j] += 128;
   };
 
-  // operand reads: limbs of row 64 wm + 16 u + c at aread[q] + 2048 u, codes of
-  // image row 64 wn + 16 t + c at cread[q] + 2048 t
+  // operand reads: limbs of row 16 u + c at aread[q] + 2048 u, words of row
+  // 16 t + c at cread[q] + 512 t, its scales at sread + 128 t
   uint32_t aread[2], cread[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int ra = 64 * wm + c, rc = 64 * wn + c;
-    aread[q] = uint32_t(ra * 128 + 16 * ((4 * q + R) ^ ((ra >> 1) & 7)));
-    cread[q] = uint32_t(rc * 128 + 16 * ((4 * q + R) ^ ((rc >> 1) & 7)));
+    aread[q] = uint32_t(c * 128 + 16 * ((4 * q + R) ^ ((c >> 1) & 7)));
+    cread[q] = uint32_t(kW + 2048 * wave + 32 * c + 16 * (q ^ (c >> 3)) + 4 * R);
   }
-  float acc[4][4][4];
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[u][t][r] = 0.0f;
+  const uint32_t sread = uint32_t(kS + 512 * wave + 8 * c);
+
+  floatx4 acc[U][4];
   const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  auto products = [&](const unsigned char *img, const unsigned char *cimg, const float *simg) {
-    float2 s[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-      s[t] = *reinterpret_cast<const float2 *>(simg + 2 * (64 * wn + 16 * t + c));
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[u][t] = zero;
+
+  // The scales times kFold.  Groups whose scale cannot be folded in are done
+  // here (none in an ordinary stage: one look at the largest and the least of
+  // the wave's) and left with 0.
+  auto fold_scales = [&](const unsigned char *img, int p, float2 (&s)[4]) {
+    float most = 0.0f, least = 1.0f;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      s[t].x *= kFold;
+      s[t].y *= kFold;
+      most = fmaxf(fmaxf(most, fabsf(s[t].x)), fabsf(s[t].y));
+      least = fminf(fminf(least, fabsf(s[t].x)), fabsf(s[t].y));
+    }
+    if (__ballot(!(most < 4096.0f) | (least < 0x1p-10f)) == 0) return;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      half8_t x[L][4], b[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) b[t] = *reinterpret_cast<const half8_t *>(cimg + cread[q] + 2048 * t);
+      for (int t = 0; t < 4; ++t) {
+        float &m = q == 0 ? s[t].x : s[t].y;
+        if (__ballot(!foldable(m)) == 0) continue;
+        const float sq = foldable(m) || 2 * p + q >= G ? 0.0f : m;
+        m = foldable(m) ? m : 0.0f;
+        const half8_t b =
+            nibbles_to_f16(*reinterpret_cast<const uint32_t *>(img + cread[q] + 512 * t));
 #pragma unroll
-      for (int l = 0; l < L; ++l)
+        for (int u = 0; u < U; ++u) {
+          const half8_t x = *reinterpret_cast<const half8_t *>(img + aread[q] + 2048 * u);
+          const floatx4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, b, zero, 0, 0, 0);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          x[l][u] = *reinterpret_cast<const half8_t *>(img + 16384 * l + aread[q] + 2048 * u);
+          for (int r = 0; r < 4; ++r)
+            acc[u][t][r] = sq != 0.0f ? fmaf(sq, d[r], acc[u][t][r]) : acc[u][t][r];
+        }
+      }
+    }
+  };
+  auto products = [&](const unsigned char *img, int p) {
+    float2 s[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+    for (int t = 0; t < 4; ++t) s[t] = *reinterpret_cast<const float2 *>(img + sread + 128 * t);
+    if constexpr (kFolded) fold_scales(img, p, s);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t w[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const uint32_t *>(img + cread[q] + 512 * t);
+      half8_t b[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        b[t] = nibbles_to_f16(w[t]);
+        if constexpr (kFolded) {
+          const _Float16 h = _Float16(q == 0 ? s[t].x : s[t].y);
+          b[t] = b[t] * half8_t{h, h, h, h, h, h, h, h};
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        half8_t x[L];
+#pragma unroll
+        for (int l = 0; l < L; ++l)
+          x[l] = *reinterpret_cast<const half8_t *>(img + l * kLimb + aread[q] + 2048 * u);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          floatx4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[0][u], b[t], zero, 0, 0, 0);
-          if constexpr (L == 2)
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[L - 1][u], b[t], d, 0, 0, 0);
-          const float sq = q == 0 ? s[t].x : s[t].y;
+          if constexpr (kFolded) {
+            acc[u][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[0], b[t], acc[u][t], 0, 0, 0);
+          } else {
+            floatx4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[0], b[t], zero, 0, 0, 0);
+            if constexpr (L == 2)
+              d = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[L - 1], b[t], d, 0, 0, 0);
+            const float sq = q == 0 ? s[t].x : s[t].y;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[u][t][r] = fmaf(sq, d[r], acc[u][t][r]);
+            for (int r = 0; r < 4; ++r) acc[u][t][r] = fmaf(sq, d[r], acc[u][t][r]);
+          }
         }
+      }
     }
   };
 
-  copy_stage(et_a0, 0);
-  {
-    const W w0 = load_w(0);
-    convert(w0, et_c0, et_s0);
-  }
-  W next = load_w(std::min(1, P - 1));
-  // Two stages per iteration (images by p % 2).  At a stage's start its copies
-  // have landed in this wave and its codes are written; past the barrier that
-  // holds for every wave, and every wave is past the stage before, whose images
-  // are then filled again.
-  for (int pb = 0; pb < P; pb += 2) {
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int p = pb + v;
-      if (p < P) {
-        et_wait_vm0();
-        et_wait_lgkm0();
-        et_barrier();
-        if (p + 1 < P) copy_stage(v ? et_a0 : et_a1, p + 1);
-        const W w = next;
-        next = load_w(std::min(p + 2, P - 1));
-        if (p + 1 < P) convert(w, v ? et_c0 : et_c1, v ? et_s0 : et_s1);
-        products(v ? et_a1 : et_a0, v ? et_c1 : et_c0, v ? et_s1 : et_s0);
-      }
-    }
+  // At a stage's start its copies have landed in this wave; past the barrier
+  // they have in every wave, and every wave is past the stage before, whose
+  // image is then filled again.
+  unsigned char *now = et_mem, *next = et_mem + kImage, *after = et_mem + 2 * kImage;
+  copy_stage(now, 0);
+  if (P > 1) copy_stage(next, 1);
+  for (int p = 0; p < P; ++p) {
+    if (p + 1 < P)
+      et_wait_vm<kCopies>();
+    else
+      et_wait_vm<0>();
+    et_wait_lgkm0();
+    et_barrier();
+    if (p + 2 < P) copy_stage(after, p + 2);
+    products(now, p);
+    unsigned char *const free = now;
+    now = next;
+    next = after;
+    after = free;
   }
 
   OT *y = static_cast<OT *>(a.Y);
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
+  for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int m = 64 * wm + 16 * u + 4 * R + r;
+      const int m = 16 * u + 4 * R + r;
       if (m >= rows) continue;
       const int slot = row0 + m;
       long row = slot;
       if (a.token_index) row = std::min(std::max(a.token_index[slot], 0), a.rows_x - 1);
-      const float f = a.factor[row];
+      const float f = a.factor[row] * (kFolded ? 1.0f / kFold : 1.0f);
       const long at = long(slot) * a.ldy;
       if constexpr (kSw) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const int n = n0 + 32 * wn + 16 * t + c;
+          const int n = n0 + 32 * wave + 16 * t + c;
           if (n < N) y[at + n] = from_f32<OT>(silu_mul(acc[u][t][r] * f, acc[u][t + 2][r] * f));
         }
       } else {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int n = n0 + 64 * wn + 16 * t + c;
+          const int n = n0 + 64 * wave + 16 * t + c;
           if (n < N) y[at + n] = from_f32<OT>(acc[u][t][r] * f);
         }
       }
     }
 }
 
-template <typename XT, bool kSw>
+template <typename XT, bool kSw, int U>
 hipError_t run_tile(const MoeExperts &p, hipStream_t stream) {
   using OT = typename std::conditional<kSw, XT, float>::type;
   constexpr int L = sizeof(XT) == 4 ? 2 : 1;
@@ -282,19 +357,30 @@ hipError_t run_tile(const MoeExperts &p, hipStream_t stream) {
   a.N = p.N;
   a.G = p.K / kGroup;
   a.ldy = p.ldy;
-  a.tiles_n = (p.N + (kSw ? 64 : 128) - 1) / (kSw ? 64 : 128);
-  const long tiles = long(a.tiles_n) * max_items(p.R, p.E, 128);
+  a.tiles_n = (p.N + (kSw ? 128 : 256) - 1) / (kSw ? 128 : 256);
+  const long tiles = long(a.tiles_n) * max_items(p.R, p.E, 16 * U);
   if (tiles < 1 || tiles > 0x7ffffff0L) return hipErrorInvalidValue;
   const hipError_t e = launch_limbs(p, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((experts_tile<L, OT, kSw>), dim3(unsigned((tiles + 7) / 8 * 8)),
-                     dim3(kEtThreads), 0, stream, a);
+  hipLaunchKernelGGL((experts_tile<U, L, OT, kSw, __is_same(XT, Bf16)>),
+                     dim3(unsigned((tiles + 7) / 8 * 8)), dim3(kEtThreads), 0, stream, a);
   return hipGetLastError();
+}
+
+template <typename XT, bool kSw>
+hipError_t run_tile_rows(const MoeExperts &p, hipStream_t stream) {
+  const double mean = double(p.R) / double(std::max(1, std::min(p.R, p.E)));
+#ifdef ET_U
+  return run_tile<XT, kSw, ET_U>(p, stream);
+#endif
+  if (mean <= 32) return run_tile<XT, kSw, 2>(p, stream);
+  if (mean <= 96) return run_tile<XT, kSw, 4>(p, stream);
+  return run_tile<XT, kSw, 8>(p, stream);
 }
 
 template <typename XT>
 hipError_t run_tile_type(const MoeExperts &p, hipStream_t stream) {
-  return p.swiglu ? run_tile<XT, true>(p, stream) : run_tile<XT, false>(p, stream);
+  return p.swiglu ? run_tile_rows<XT, true>(p, stream) : run_tile_rows<XT, false>(p, stream);
 }
 
 }  // namespace

@@ -75,12 +75,14 @@ def slot_lists(ids, E):
     return slots, token_index, offsets
 
 
-def terms_bound(X, qweight, scales, dtype):
+def terms_bound(X, qweight, scales, dtype, tile=False):
     """Allowed error of the sums X . W^T, element by element: the GEMM's relative
-    tolerance of the terms a kernel adds up (for bf16 x * scale * (q + 16) and
-    x * scale * 24, q the nibble), plus its absolute tolerance."""
-    if dtype != "bf16":
-        return REL_TOL * abs_gemm(X, qweight, scales) + ABS_TOL
+    tolerance of the terms a kernel adds up, plus its absolute tolerance.  For
+    bf16 the terms are x * scale * (q + 16) and x * scale * 24, q the nibble, or
+    in the tile kernel x * w with the scale and w rounded to fp16."""
+    if dtype != "bf16" or tile:
+        rel = REL_TOL + (2.01 * HALF_STEP["fp16"] if dtype == "bf16" else 0.0)
+        return rel * abs_gemm(X, qweight, scales) + ABS_TOL
     q = unpack(qweight).astype(np.float64)
     W = (q + 40.0) * np.repeat(np.abs(np.asarray(scales, np.float64)), GROUP, axis=1)
     return REL_TOL * (np.abs(np.asarray(X, np.float64)) @ W.T) + ABS_TOL
@@ -97,7 +99,7 @@ def expert_rows(offsets, E):
             yield e, slice(int(offsets[e]), int(offsets[e + 1]))
 
 
-def experts_swiglu(X, token_index, offsets, qweight, scales, dtype):
+def experts_swiglu(X, token_index, offsets, qweight, scales, dtype, tile=False):
     """(H fp64 [R][F], allowed error): silu(x . gate^T) * (x . up^T) per slot."""
     X = np.asarray(X, np.float32)  # 16-bit activations are fp32 numbers too
     E, F = qweight.shape[0], qweight.shape[1] // 2
@@ -106,7 +108,7 @@ def experts_swiglu(X, token_index, offsets, qweight, scales, dtype):
     for e, r in expert_rows(offsets, E):
         x = X[np.asarray(token_index)[r]]
         y = gemm(x, qweight[e], scales[e])
-        b = terms_bound(x, qweight[e], scales[e], dtype)
+        b = terms_bound(x, qweight[e], scales[e], dtype, tile)
         g, u, eg, eu = y[:, :F], y[:, F:], b[:, :F], b[:, F:]
         sg = np.abs(silu(g))
         H[r] = silu(g) * u
@@ -115,7 +117,7 @@ def experts_swiglu(X, token_index, offsets, qweight, scales, dtype):
     return H, tol + rounded(np.abs(H) + tol, dtype)
 
 
-def experts_combine(H, offsets, qweight, scales, slots, weights, dtype):
+def experts_combine(H, offsets, qweight, scales, slots, weights, dtype, tile=False):
     """(Y fp64 [T][N], allowed error): sum_j weights[t][j] * (H[slots[t][j]] . W_e^T)."""
     H = np.asarray(H, np.float32)
     weights = np.asarray(weights, np.float64)
@@ -124,7 +126,7 @@ def experts_combine(H, offsets, qweight, scales, slots, weights, dtype):
     tol = np.zeros_like(D)
     for e, r in expert_rows(offsets, E):
         D[r] = gemm(H[r], qweight[e], scales[e])
-        tol[r] = terms_bound(H[r], qweight[e], scales[e], dtype)
+        tol[r] = terms_bound(H[r], qweight[e], scales[e], dtype, tile)
     T, topk = np.asarray(slots).shape
     Y, err, size = np.zeros((T, N)), np.zeros((T, N)), np.zeros((T, N))
     for t in range(T):

@@ -53,12 +53,23 @@ def on(dev, *arrays):
     return [torch.from_numpy(np.ascontiguousarray(a)).to(dev) for a in arrays]
 
 
+def tile(R, E):
+    return pkg.w4a16_experts_kernel(R, E) == pkg.W4A16_EXPERTS_TILE
+
+
 def within(got, want, tol, what):
+    """got within tol of want; values past the type's largest are stored as infinities"""
+    most = torch.finfo(got.dtype).max
     got = got.float().cpu().numpy().astype(np.float64)
-    assert np.all(np.isfinite(got))
-    err = np.abs(got - want)
-    say(f"  {what}: max err/bound {np.max(err / tol) if err.size else 0:.3e}")
-    assert np.all(err <= tol)
+    over = np.abs(want) - tol > most  # certain to overflow
+    assert np.all(got[over] == np.sign(want[over]) * np.inf)
+    near = ~over & (np.abs(want) + tol > most) & np.isinf(got)
+    assert np.all(np.sign(got[near]) == np.sign(want[near]))
+    rest = ~over & ~near
+    assert np.all(np.isfinite(got[rest]))
+    err = np.abs(got[rest] - want[rest])
+    say(f"  {what}: max err/bound {np.max(err / tol[rest]) if err.size else 0:.3e}")
+    assert np.all(err <= tol[rest])
 
 
 def run_swiglu(dev, counts, T, F, K, dtype, seed, spare=0):
@@ -79,7 +90,7 @@ def run_swiglu(dev, counts, T, F, K, dtype, seed, spare=0):
     torch.cuda.synchronize()
     assert out is Hd
     assert torch.all(buf[:pad] == 77) and torch.all(buf[pad + len(tok) * F:] == 77)
-    H, tol = oracle.experts_swiglu(X, tok, off, qw, sc, dtype)
+    H, tol = oracle.experts_swiglu(X, tok, off, qw, sc, dtype, tile(R, E))
     within(Hd[:len(tok)], H, tol, f"swiglu {dtype}")
     again = pkg.w4a16_gemm_grouped_swiglu(Xd, tokd, offd, qwd, scd)
     assert torch.equal(again[:len(tok)], Hd[:len(tok)])
@@ -147,7 +158,7 @@ def test_combine_shapes(dev, T, topk, E, N, K, live, dtype):
     Yd = pkg.w4a16_gemm_grouped_combine(Hd, *args, Y=buf[pad:pad + T * N].view(T, N))
     torch.cuda.synchronize()
     assert torch.all(buf[:pad] == 77) and torch.all(buf[pad + T * N:] == 77)
-    Y, tol = oracle.experts_combine(Hv, off, qw, sc, slots, w, dtype)
+    Y, tol = oracle.experts_combine(Hv, off, qw, sc, slots, w, dtype, tile(T * topk, E))
     within(Yd, Y, tol, f"combine {dtype}")
     assert torch.equal(pkg.w4a16_gemm_grouped_combine(Hd, *args), Yd)
 
@@ -185,11 +196,13 @@ def test_layer(dev, T, dtype):
         slots, tok, off = oracle.slot_lists(ids, E)
         assert np.array_equal(r.slots.cpu().numpy(), slots)
         m = off[-1]
-        want, tol = oracle.experts_swiglu(x, tok[:m], off, gq, gs, dtype)
+        big = tile(T * topk, E)
+        want, tol = oracle.experts_swiglu(x, tok[:m], off, gq, gs, dtype, big)
         within(H[:m], want, tol, "layer H")
         Hv = np.zeros((T * topk, F), np.float32)
         Hv[:m] = H[:m].float().cpu().numpy()
-        want, tol = oracle.experts_combine(Hv, off, dq, ds, slots, r.weights.cpu().numpy(), dtype)
+        want, tol = oracle.experts_combine(Hv, off, dq, ds, slots, r.weights.cpu().numpy(), dtype,
+                                           big)
         within(Y, want, tol, "layer Y")
         assert torch.all(Y[live:] == 0)
 
@@ -263,8 +276,30 @@ def test_far_magnitudes(dev):
             t = torch.from_numpy(x.astype(np.float32)).to(TYPES[dtype])
             tokd, offd, qwd, scd = on(dev, tok, off, qw, sc2)
             H = pkg.w4a16_gemm_grouped_swiglu(t.to(dev), tokd, offd, qwd, scd)
-            want, tol = oracle.experts_swiglu(t.float().numpy(), tok, off, qw, sc2, dtype)
+            want, tol = oracle.experts_swiglu(t.float().numpy(), tok, off, qw, sc2, dtype,
+                                              tile(2 * per, E))
             within(H, want, tol, f"far {dtype} {per}")
+
+
+@pytest.mark.parametrize("K", [32, 160, 512])
+def test_scales_out_of_fp16_range(dev, K):
+    """Groups whose scaled weights fp16 does not hold, among ordinary ones: tiny,
+    huge, negative and zero scales, in one stage or another of the tile kernel."""
+    E, F, T = 2, 70, 90
+    rng = np.random.default_rng(K)
+    tok, off = lists_of([100, 130], T, rng)
+    qw, sc = weights_of(rng, E, 2 * F, K)
+    sc[0, 5, 0] = 5.0
+    sc[0, 6, 0] = -3e-3
+    sc[0, 7, K // 32 - 1] = 3e-8
+    sc[0, 80, K // 64] = 100.0
+    sc[1, 100] = 1e-9
+    sc[1, 139, K // 32 - 1] = 0.0
+    for dtype in TYPES:
+        Xd, X = activations(rng, T, K, dtype)
+        H = pkg.w4a16_gemm_grouped_swiglu(Xd, *on(dev, tok, off, qw, sc))
+        want, tol = oracle.experts_swiglu(X, tok, off, qw, sc, dtype, True)
+        within(H, want, tol, f"scales {dtype} {K}")
 
 
 def test_binding_refusals(dev):
