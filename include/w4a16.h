@@ -536,13 +536,15 @@ int w4a16_moe_route(const void *logits, const float *bias, const int32_t *num_to
 
 /* Kernels behind w4a16_gemm_grouped_swiglu and w4a16_gemm_grouped_combine. */
 #define W4A16_EXPERTS_SKINNY 1 /* few slots per expert: weights and activations from memory to
-                                  registers, K split over the 8 waves of a workgroup */
-#define W4A16_EXPERTS_TILE 2   /* many: 128 x 128 tiles on fp16 limbs of the activations
+                                  registers, K split over up to 4 waves */
+#define W4A16_EXPERTS_TILE 2   /* many: tiles of 32 to 128 slots on fp16 limbs of the activations
                                   (made in the workspace) */
 
-/* The kernel for R slots over E experts (one of W4A16_EXPERTS_*), 0 for
- * extents that are refused or a no-op.  Host only. */
-int w4a16_experts_kernel(int64_t R, int64_t E);
+/* The kernel for R slots over E experts (one of W4A16_EXPERTS_*): the tile past
+ * 36 slots per expert (of the fewer of R and E), with fp32 activations past 14.
+ * 0 for extents that are refused or a no-op, and for an unknown dtype.  Host
+ * only. */
+int w4a16_experts_kernel(int64_t R, int64_t E, int32_t dtype);
 
 /* Workspace bytes of w4a16_gemm_grouped_swiglu (0 for the skinny kernel on
  * 16-bit activations and for extents it refuses).  Host only. */

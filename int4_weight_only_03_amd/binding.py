@@ -94,7 +94,7 @@ _SIGS = {
                         [ctypes.c_int64] * 2 + [ctypes.c_int32] * 2 +
                         [ctypes.c_float, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
                          ctypes.c_void_p], ctypes.c_int),
-    "w4a16_experts_kernel": ([ctypes.c_int64] * 2, ctypes.c_int),
+    "w4a16_experts_kernel": ([ctypes.c_int64] * 2 + [ctypes.c_int32], ctypes.c_int),
     "w4a16_grouped_swiglu_workspace_bytes": ([ctypes.c_int64] * 5 + [ctypes.c_int32],
                                              ctypes.c_size_t),
     "w4a16_gemm_grouped_swiglu": ([ctypes.c_void_p] * 6 + [ctypes.c_int64] * 5 +

@@ -133,9 +133,9 @@ int w4a16_moe_route(const void *logits, const float *bias, const int32_t *num_to
   return status(w4a16::launch_route(r, workspace, reinterpret_cast<hipStream_t>(stream)));
 }
 
-int w4a16_experts_kernel(int64_t R, int64_t E) {
-  if (R <= 0 || E <= 0 || R > W4A16_MAX_M || E > 65535) return 0;
-  return w4a16::experts_kernel(long(R), long(E));
+int w4a16_experts_kernel(int64_t R, int64_t E, int32_t dtype) {
+  if (R <= 0 || E <= 0 || R > W4A16_MAX_M || E > 65535 || !dtype_ok(dtype)) return 0;
+  return w4a16::experts_kernel(long(R), long(E), dtype);
 }
 
 size_t w4a16_grouped_swiglu_workspace_bytes(int64_t T, int64_t R, int64_t E, int64_t F, int64_t K,

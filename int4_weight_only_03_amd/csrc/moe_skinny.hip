@@ -30,9 +30,9 @@
 // each of the step's 4 groups, its B operand.  Its A operand is k = 8R .. 8R+7
 // of the slot in tile row c, D holds tile rows 4R .. 4R+3 of W row c.  Slot i
 // of 16 stands in tile row 4 (i % 4) + i / 4, so that up to 4 MR slots fill only
-// the first MR of D's registers and the rest cost no scale FMA.
+// the first MR of D's registers and the others cost no scale FMA.
 //
-// A wave takes MT x 16 (or 4 MR) slots of one expert by NT x 16 rows of W (gate
+// A wave takes 4 MR slots of one expert by NT x 16 rows of W (gate
 // tiles, then the up tiles of the same outputs) over blocks of 16 groups; KW
 // waves of a workgroup share a tile, taking blocks in turn, and their sums are
 // added in wave order in LDS.  The next block's weights fly while a block is
@@ -101,14 +101,13 @@ __device__ __forceinline__ long row_of(const ExpertArgs &a, int slot) {
 
 // kSw: W has 2N rows, Y is XT; else Y is fp32.  P: steps in flight per wave (2
 // or 4).  kOcc: waves per SIMD.
-template <typename XT, int MT, int MR, int NT, int KW, int P, int kOcc, bool kSw>
+template <typename XT, int MR, int NT, int KW, int P, int kOcc, bool kSw>
 __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a) {
   constexpr int NO = kSw ? NT / 2 : NT;
-  constexpr int B = MT > 1 ? 16 * MT : 4 * MR;  // slots of an item
+  constexpr int B = 4 * MR;  // slots of an item
   constexpr bool kLimbs = sizeof(XT) == 4;
-  static_assert(MT == 1 || MR == 4, "several slot tiles are full ones");
   // per wave: a block's scales, row n of the tile at 64 n; at the end the sums
-  constexpr int kTile = MT * MR * NT * 64;
+  constexpr int kTile = MR * NT * 64;
   constexpr int kWaveLds = KW > 1 && kTile > NT * 256 ? kTile : NT * 256;
   __shared__ __align__(16) float es_lds[kEsWaves * kWaveLds];
   const int lane = threadIdx.x & 63;
@@ -122,13 +121,11 @@ __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a)
   const ExpertItem it = find_item(a.offsets, a.E, a.R, B, item);
   const int G = a.G, N = a.N;
 
-  float acc[MT][NT][MR];
+  float acc[NT][MR];
 #pragma unroll
-  for (int u = 0; u < MT; ++u)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int r = 0; r < MR; ++r) acc[u][t][r] = 0.0f;
+    for (int r = 0; r < MR; ++r) acc[t][r] = 0.0f;
 
   const int blocks = (G + kEsBlock - 1) / kEsBlock;
   const int mine = it.e >= 0 && blocks > kw ? (blocks - kw + KW - 1) / KW : 0;
@@ -147,12 +144,9 @@ __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a)
       soff[t] = uint32_t(std::min(n0 + 16 * t + lane / 4, N - 1) - n0) * uint32_t(G) * 4u;
     }
     // the activations (slots past the item repeat its last)
-    const int slot = (c >> 2) + 4 * (MT > 1 ? (c & 3) : std::min(c & 3, MR - 1));
-    const char *xrow[MT];
-#pragma unroll
-    for (int u = 0; u < MT; ++u)
-      xrow[u] = static_cast<const char *>(a.X) +
-                2 * (row_of(a, it.row0 + std::min(16 * u + slot, it.rows - 1)) * a.ldx + 8 * R);
+    const int slot = (c >> 2) + 4 * std::min(c & 3, MR - 1);
+    const char *const xrow = static_cast<const char *>(a.X) +
+                             2 * (row_of(a, it.row0 + std::min(slot, it.rows - 1)) * a.ldx + 8 * R);
     const long plane = 2 * long(a.rows_x) * a.ldx;
 
     // step j of block b; groups past G read group G - 1 and are left out later.
@@ -161,7 +155,7 @@ __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a)
     // for every weight asked for before them.
     struct Ops {
       u32x4m w[NT];
-      XChunk<XT> x[MT][4];
+      XChunk<XT> x[4];
     };
     auto load = [&](Ops &o, int b, int j) {
       const uint32_t gw = 16u * uint32_t(std::min(b * kEsBlock + 4 * j + R, G - 1));
@@ -169,14 +163,11 @@ __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a)
       for (int t = 0; t < NT; ++t)
         o.w[t] = *reinterpret_cast<const u32x4m *>(wbase + (t < NO ? 0 : up_w) + (woff[t % NO] + gw));
 #pragma unroll
-      for (int u = 0; u < MT; ++u)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const long g = 64 * long(std::min(b * kEsBlock + 4 * j + q, G - 1));
-          o.x[u][q].v[0] = *reinterpret_cast<const u32x4m *>(xrow[u] + g);
-          if constexpr (kLimbs)
-            o.x[u][q].v[1] = *reinterpret_cast<const u32x4m *>(xrow[u] + plane + g);
-        }
+      for (int q = 0; q < 4; ++q) {
+        const long g = 64 * long(std::min(b * kEsBlock + 4 * j + q, G - 1));
+        o.x[q].v[0] = *reinterpret_cast<const u32x4m *>(xrow + g);
+        if constexpr (kLimbs) o.x[q].v[1] = *reinterpret_cast<const u32x4m *>(xrow + plane + g);
+      }
     };
     // Scales of block b: lane l takes 4 groups of row l / 4 of each tile, the
     // last shares moved back to end at G.
@@ -218,34 +209,30 @@ __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a)
 
     const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
     auto group = [&](const Ops &o, const float4 (&sc)[NT], int q) {
+      const u32x4m xa = kLimbs ? o.x[q].v[0] : interleave8(o.x[q].v[0]);
+      floatx4 d0 = zero;
+      if constexpr (__is_same(XT, Bf16)) {
+        const bf16x8 off = __builtin_bit_cast(
+            bf16x8, u32x4m{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u});  // -24
+        d0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xa), off, zero, 0, 0,
+                                                     0);
+      }
 #pragma unroll
-      for (int u = 0; u < MT; ++u) {
-        const u32x4m xa = kLimbs ? o.x[u][q].v[0] : interleave8(o.x[u][q].v[0]);
-        floatx4 d0 = zero;
+      for (int t = 0; t < NT; ++t) {
+        floatx4 d;
         if constexpr (__is_same(XT, Bf16)) {
-          const bf16x8 off = __builtin_bit_cast(
-              bf16x8, u32x4m{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u});  // -24
-          d0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xa), off, zero, 0,
-                                                       0, 0);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xa),
+                                                      nibbles_to_bf16_16(o.w[t][q]), d0, 0, 0, 0);
+        } else {
+          const half8_t b = nibbles_to_f16(o.w[t][q]);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, xa), b, zero, 0, 0, 0);
+          if constexpr (kLimbs)
+            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                __builtin_bit_cast(half8_t, o.x[q].v[sizeof(XT) / 4]), b, d, 0, 0, 0);
         }
+        const float s = q == 0 ? sc[t].x : q == 1 ? sc[t].y : q == 2 ? sc[t].z : sc[t].w;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          floatx4 d;
-          if constexpr (__is_same(XT, Bf16)) {
-            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xa),
-                                                        nibbles_to_bf16_16(o.w[t][q]), d0, 0, 0, 0);
-          } else {
-            const half8_t b = nibbles_to_f16(o.w[t][q]);
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, xa), b, zero, 0,
-                                                       0, 0);
-            if constexpr (kLimbs)
-              d = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                  __builtin_bit_cast(half8_t, o.x[u][q].v[sizeof(XT) / 4]), b, d, 0, 0, 0);
-          }
-          const float s = q == 0 ? sc[t].x : q == 1 ? sc[t].y : q == 2 ? sc[t].z : sc[t].w;
-#pragma unroll
-          for (int r = 0; r < MR; ++r) acc[u][t][r] = fmaf(s, d[r], acc[u][t][r]);
-        }
+        for (int r = 0; r < MR; ++r) acc[t][r] = fmaf(s, d[r], acc[t][r]);
       }
     };
     // left: groups of the step that there are
@@ -300,69 +287,60 @@ __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a)
     // sums of the tile's waves, in their order, on the first of them (each wave
     // is past its own words)
 #pragma unroll
-    for (int u = 0; u < MT; ++u)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < MR; ++r) mem[((u * NT + t) * MR + r) * 64 + lane] = acc[u][t][r];
+      for (int r = 0; r < MR; ++r) mem[(t * MR + r) * 64 + lane] = acc[t][r];
     __syncthreads();
     if (kw != 0) return;
 #pragma unroll
-    for (int u = 0; u < MT; ++u)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int r = 0; r < MR; ++r)
 #pragma unroll
-        for (int r = 0; r < MR; ++r)
-#pragma unroll
-          for (int k = 1; k < KW; ++k)
-            acc[u][t][r] += mem[k * kWaveLds + ((u * NT + t) * MR + r) * 64 + lane];
+        for (int k = 1; k < KW; ++k) acc[t][r] += mem[k * kWaveLds + (t * MR + r) * 64 + lane];
   }
   if (it.e < 0) return;
 #pragma unroll
-  for (int u = 0; u < MT; ++u)
+  for (int r = 0; r < MR; ++r) {
+    const int m = R + 4 * r;
+    if (m >= it.rows) continue;
+    float f = 1.0f;
+    if constexpr (kLimbs) f = a.factor[row_of(a, it.row0 + m)];
+    const long y = long(it.row0 + m) * a.ldy;
 #pragma unroll
-    for (int r = 0; r < MR; ++r) {
-      const int m = 16 * u + R + 4 * r;
-      if (m >= it.rows) continue;
-      float f = 1.0f;
-      if constexpr (kLimbs) f = a.factor[row_of(a, it.row0 + m)];
-      const long y = long(it.row0 + m) * a.ldy;
-#pragma unroll
-      for (int t = 0; t < NO; ++t) {
-        const int n = n0 + 16 * t + c;
-        if (n >= N) continue;
-        const float g = acc[u][t][r] * f;
-        if constexpr (kSw)
-          static_cast<XT *>(a.Y)[y + n] = from_f32<XT>(silu_mul(g, acc[u][t + NO][r] * f));
-        else
-          static_cast<float *>(a.Y)[y + n] = g;
-      }
+    for (int t = 0; t < NO; ++t) {
+      const int n = n0 + 16 * t + c;
+      if (n >= N) continue;
+      const float g = acc[t][r] * f;
+      if constexpr (kSw)
+        static_cast<XT *>(a.Y)[y + n] = from_f32<XT>(silu_mul(g, acc[t + NO][r] * f));
+      else
+        static_cast<float *>(a.Y)[y + n] = g;
     }
+  }
 }
 
-template <typename XT, int MT, int MR, int NT, int KW, int P, int kOcc, bool kSw>
+template <typename XT, int MR, int NT, int KW, int P, int kOcc, bool kSw>
 hipError_t run_skinny(ExpertArgs a, hipStream_t stream) {
   constexpr int NO = kSw ? NT / 2 : NT;
-  constexpr int B = MT > 1 ? 16 * MT : 4 * MR;
   a.tiles_n = (a.N + 16 * NO - 1) / (16 * NO);
-  const long tiles = long(a.tiles_n) * max_items(a.R, a.E, B);
+  const long tiles = long(a.tiles_n) * max_items(a.R, a.E, 4 * MR);
   const long blocks = (tiles * KW + kEsWaves - 1) / kEsWaves;
   if (blocks < 1 || blocks > 0x7fffffffL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((experts_skinny<XT, MT, MR, NT, KW, P, kOcc, kSw>), dim3(unsigned(blocks)),
+  hipLaunchKernelGGL((experts_skinny<XT, MR, NT, KW, P, kOcc, kSw>), dim3(unsigned(blocks)),
                      dim3(kEsThreads), 0, stream, a);
   return hipGetLastError();
 }
 
 template <typename XT, bool kSw, int KW>
 hipError_t run_skinny_rows(const ExpertArgs &a, hipStream_t stream) {
-  constexpr bool kLimbs = sizeof(XT) == 4;
-  switch (experts_skinny_rows(a.R, a.E)) {
-    case 4: return run_skinny<XT, 1, 1, 4, KW, 2, 2, kSw>(a, stream);
-    case 8: return run_skinny<XT, 1, 2, 4, KW, 2, 2, kSw>(a, stream);
-    case 16: return run_skinny<XT, 1, 4, 4, KW, 2, 2, kSw>(a, stream);
-    case 32: return run_skinny<XT, 2, 4, 2, KW, kLimbs ? 1 : 2, 2, kSw>(a, stream);
-    default: return run_skinny<XT, 4, 4, 2, KW, 1, 2, kSw>(a, stream);
-  }
+  // slots per item: enough for one item of most experts (32 experts of 2 x 1024
+  // x 4096, mean 4: 47 us with 8, 41 with 16; with row tiles of 32 and 64
+  // slots means of 12 to 24 took 72 to 91 us, with several items of 16 58 to 75)
+  const double mean = double(a.R) / double(std::max(1, std::min(a.R, a.E)));
+  if (mean <= 1.25) return run_skinny<XT, 1, 4, KW, 2, 2, kSw>(a, stream);
+  if (mean <= 3.0) return run_skinny<XT, 2, 4, KW, 2, 2, kSw>(a, stream);
+  return run_skinny<XT, 4, 4, KW, 2, 2, kSw>(a, stream);
 }
 
 template <typename XT, bool kSw>
@@ -378,12 +356,6 @@ hipError_t run_skinny_type(const ExpertArgs &a, hipStream_t stream) {
 }
 
 }  // namespace
-
-// slots per item: enough for one item of most experts
-int experts_skinny_rows(long R, long E) {
-  const double mean = double(R) / double(std::max(1L, std::min(R, E)));
-  return mean <= 1.25 ? 4 : mean <= 4.0 ? 8 : mean <= 10.0 ? 16 : mean <= 24.0 ? 32 : 64;
-}
 
 hipError_t launch_experts_skinny(const MoeExperts &p, hipStream_t stream) {
   ExpertArgs a;

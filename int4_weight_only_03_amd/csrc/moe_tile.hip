@@ -1,5 +1,5 @@
 // Experts' W4A16 products for many slots per expert (prompts): the products of
-// moe_skinny.hip in 128 x 128 tiles on the fp16 matrix instructions.
+// moe_skinny.hip in tiles of up to 128 slots by 256 rows on the fp16 matrix instructions.
 //
 // The activations come as fp16 limbs that moe_limbs.hip makes in the workspace,
 // once for all the tiles that read them: one limb for fp16 and bf16, two for
@@ -24,9 +24,12 @@
 //         fp16's range: its group counts as 0 there, and a stage with such a
 //         group adds its exact codes' products, scaled in fp32, by themselves.
 //
-// Stages of two groups.  Limbs (gathered rows, 128 bytes each), weight words and
-// scales come to LDS by direct copies, two stages ahead, into three images; a
-// stage has one barrier.  A wave copies the weights and scales of its own rows.
+// Stages of two groups.  Limbs (gathered rows, 128 bytes a stage) come to LDS by
+// direct copies one stage ahead, weight words and scales for two stages at once
+// (64 and 16 bytes a row), two stages ahead; both have two images, and a stage
+// one barrier.  A wave copies the weights and scales of its own rows.  Copied
+// stage by stage, 32 and 8 bytes a row, their requests held up all others (32
+// experts of 2 x 2048 x 7168, 16384 slots in bf16: 1127 us; so 1034).
 //
 // Tiles are dealt so that each XCD works a contiguous run of them (the
 // hardware deals workgroups round-robin over the 8 XCDs), row blocks of an
@@ -94,18 +97,20 @@ struct TileArgs {
 // U: row tiles of 16 slots, L limbs, OT the output type (kSw: the activations'
 // type, else fp32), kFolded: weights with their scales.
 template <int U, int L, typename OT, bool kSw, bool kFolded>
-__global__ void __launch_bounds__(kEtThreads, U == 8 && L == 2 ? 1 : 2) experts_tile(TileArgs a) {
+__global__ void __launch_bounds__(kEtThreads, 2) experts_tile(TileArgs a) {
   static_assert(!kFolded || L == 1, "folded weights have fp16's precision");
-  // An image of a stage (64 k).
-  // Limbs: row r at 128 r, logical chunk x (16 bytes: 8 values of one group's
-  // block x % 4, group x / 4) at chunk x ^ ((r / 2) % 8), so that the 16 rows an
-  // operand read touches fall in distinct banks.
-  // Weights: W row n at 32 n, its 16 bytes of group q at half q ^ ((n / 8) % 2),
-  // for the same reason.  Scales: group q of row n at 8 n + 4 q.
+  // Limbs of a stage (64 k): row r at 128 r, logical chunk x (16 bytes: 8 values
+  // of one group's block x % 4, group x / 4) at chunk x ^ ((r / 2) % 8), so that
+  // the 16 rows an operand read touches fall in distinct banks.
+  // Weights of two stages: W row n at 64 n, its 16 bytes of group q (0..3) at
+  // chunk q ^ ((n / 4) % 4), for the same reason.  Their scales: group q of row n
+  // at 16 n + 4 q.
   constexpr int kRows = 16 * U, kLimb = kRows * 128;
-  constexpr int kW = L * kLimb, kS = kW + 8192, kImage = kS + 2048;
-  __shared__ __align__(16) unsigned char et_mem[3 * kImage];
-  constexpr int kCopies = L * (U / 2) + 4;  // of a wave and stage
+  constexpr int kA = L * kLimb, kW = 16384, kS = 4096;
+  __shared__ __align__(16) unsigned char et_mem[2 * (kA + kW + kS)];
+  unsigned char *const a_mem = et_mem, *const w_mem = et_mem + 2 * kA,
+                      *const s_mem = w_mem + 2 * kW;
+  constexpr int kPairCopies = 8;            // weights and scales, of a wave
   constexpr int NO = kSw ? 128 : 256;       // outputs per tile
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -155,55 +160,59 @@ __global__ void __launch_bounds__(kEtThreads, U == 8 && L == 2 ? 1 : 2) experts_
       n = std::min(n0 + 64 * wave + i, N - 1);
     return n + long(it.e) * (kSw ? 2 * long(N) : long(N));
   };
-  // Weight copies j = 0, 1: lane i writes 16 B: row 32 j + i / 2, half i % 2.
-  // Scale copies: lane i writes 4 B: row 32 j + i / 2, group i % 2.
-  const unsigned char *wsrc[2];
-  const float *ssrc[2];
-  int wq[2];  // the lane's group of the stage
+  // Weight copies j = 0..3: lane i writes 16 B: row 16 j + i / 4, chunk i % 4.
+  // Scale copies: lane i writes 4 B: row 16 j + i / 4, group i % 4.
+  const unsigned char *wsrc[4];
+  const float *ssrc[4];
+  int wq[4];  // the lane's group of the two stages
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int i = 32 * j + lane / 2;
-    wq[j] = (lane & 1) ^ ((i >> 3) & 1);
-    wsrc[j] = a.qw + w_row(i) * G * 16 + 16 * wq[j];
-    ssrc[j] = a.sc + w_row(i) * G + (lane & 1);
+  for (int j = 0; j < 4; ++j) {
+    const int i = 16 * j + lane / 4;
+    wq[j] = (lane & 3) ^ ((i >> 2) & 3);
+    wsrc[j] = a.qw + (w_row(i) * G + wq[j]) * 16;
+    ssrc[j] = a.sc + w_row(i) * G + (lane & 3);
   }
   const int P = (G + 1) / 2;
-  // stage p into an image; called for the stages in order
-  auto copy_stage = [&](unsigned char *img, int p) {
-    // an odd G's last stage has one group: the other half reads it again (its
-    // limbs are 0)
-    if (2 * p + 1 >= G) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        wsrc[j] -= wq[j] ? 16 : 0;
-        ssrc[j] -= lane & 1;
-      }
-    }
+  // limbs of a stage; called for the stages in order
+  auto copy_limbs = [&](unsigned char *img) {
 #pragma unroll
     for (int l = 0; l < L; ++l)
 #pragma unroll
       for (int j = 0; j < U / 2; ++j)
         et_copy16(asrc[j] + l * plane, img + l * kLimb + 1024 * (wave * (U / 2) + j));
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      et_copy16(wsrc[j], img + kW + 2048 * wave + 1024 * j);
-      et_copy4(ssrc[j], img + kS + 512 * wave + 256 * j);
-      wsrc[j] += 32;
-      ssrc[j] += 2;
-    }
-#pragma unroll
     for (int j = 0; j < U / 2; ++j) asrc[j] += 128;
   };
+  // weights and scales of stages 2 k and 2 k + 1; called in order
+  auto copy_pair = [&](unsigned char *wimg, unsigned char *simg, int k) {
+    if (4 * k + 4 > G) {
+      // groups past G read group G - 1 again (their limbs are 0)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        wsrc[j] -= 16 * std::max(4 * k + wq[j] - (G - 1), 0);
+        ssrc[j] -= std::max(4 * k + (lane & 3) - (G - 1), 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      et_copy16(wsrc[j], wimg + 4096 * wave + 1024 * j);
+      et_copy4(ssrc[j], simg + 1024 * wave + 256 * j);
+      wsrc[j] += 64;
+      ssrc[j] += 4;
+    }
+  };
 
-  // operand reads: limbs of row 16 u + c at aread[q] + 2048 u, words of row
-  // 16 t + c at cread[q] + 512 t, its scales at sread + 128 t
+  // operand reads: limbs of row 16 u + c at aread[q] + 2048 u; words of row
+  // 16 t + c, group q, at cread[q] + 1024 t (^ 32 for the images' second stage);
+  // its scales at sread + 256 t (+ 8)
   uint32_t aread[2], cread[2];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = 0; q < 2; ++q)
     aread[q] = uint32_t(c * 128 + 16 * ((4 * q + R) ^ ((c >> 1) & 7)));
-    cread[q] = uint32_t(kW + 2048 * wave + 32 * c + 16 * (q ^ (c >> 3)) + 4 * R);
-  }
-  const uint32_t sread = uint32_t(kS + 512 * wave + 8 * c);
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    cread[q] = uint32_t(4096 * wave + 64 * c + 16 * (q ^ (c >> 2)) + 4 * R);
+  const uint32_t sread = uint32_t(1024 * wave + 16 * c);
 
   floatx4 acc[U][4];
   const floatx4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -215,7 +224,9 @@ __global__ void __launch_bounds__(kEtThreads, U == 8 && L == 2 ? 1 : 2) experts_
   // The scales times kFold.  Groups whose scale cannot be folded in are done
   // here (none in an ordinary stage: one look at the largest and the least of
   // the wave's) and left with 0.
-  auto fold_scales = [&](const unsigned char *img, int p, float2 (&s)[4]) {
+  auto fold_scales = [&](const unsigned char *img, const unsigned char *wimg, int p,
+                         float2 (&s)[4]) {
+    const uint32_t h = p & 1;
     float most = 0.0f, least = 1.0f;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(kEtThreads, U == 8 && L == 2 ? 1 : 2) experts_
         const float sq = foldable(m) || 2 * p + q >= G ? 0.0f : m;
         m = foldable(m) ? m : 0.0f;
         const half8_t b =
-            nibbles_to_f16(*reinterpret_cast<const uint32_t *>(img + cread[q] + 512 * t));
+            nibbles_to_f16(*reinterpret_cast<const uint32_t *>(wimg + (cread[q] ^ 32 * h) + 1024 * t));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const half8_t x = *reinterpret_cast<const half8_t *>(img + aread[q] + 2048 * u);
@@ -246,23 +257,27 @@ __global__ void __launch_bounds__(kEtThreads, U == 8 && L == 2 ? 1 : 2) experts_
       }
     }
   };
-  auto products = [&](const unsigned char *img, int p) {
+  auto products = [&](const unsigned char *img, const unsigned char *wimg,
+                      const unsigned char *simg, int p) {
+    const uint32_t h = p & 1;
     float2 s[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) s[t] = *reinterpret_cast<const float2 *>(img + sread + 128 * t);
-    if constexpr (kFolded) fold_scales(img, p, s);
+    for (int t = 0; t < 4; ++t)
+      s[t] = *reinterpret_cast<const float2 *>(simg + sread + 256 * t + 8 * h);
+    if constexpr (kFolded) fold_scales(img, wimg, p, s);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       uint32_t w[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const uint32_t *>(img + cread[q] + 512 * t);
+      for (int t = 0; t < 4; ++t)
+        w[t] = *reinterpret_cast<const uint32_t *>(wimg + (cread[q] ^ 32 * h) + 1024 * t);
       half8_t b[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         b[t] = nibbles_to_f16(w[t]);
         if constexpr (kFolded) {
-          const _Float16 h = _Float16(q == 0 ? s[t].x : s[t].y);
-          b[t] = b[t] * half8_t{h, h, h, h, h, h, h, h};
+          const _Float16 f = _Float16(q == 0 ? s[t].x : s[t].y);
+          b[t] = b[t] * half8_t{f, f, f, f, f, f, f, f};
         }
       }
 #pragma unroll
@@ -290,23 +305,23 @@ __global__ void __launch_bounds__(kEtThreads, U == 8 && L == 2 ? 1 : 2) experts_
 
   // At a stage's start its copies have landed in this wave; past the barrier
   // they have in every wave, and every wave is past the stage before, whose
-  // image is then filled again.
-  unsigned char *now = et_mem, *next = et_mem + kImage, *after = et_mem + 2 * kImage;
-  copy_stage(now, 0);
-  if (P > 1) copy_stage(next, 1);
+  // limbs' image is then filled again, and past the two stages before an even
+  // stage, whose weights' image is.
+  copy_limbs(a_mem);
+  copy_pair(w_mem, s_mem, 0);
   for (int p = 0; p < P; ++p) {
-    if (p + 1 < P)
-      et_wait_vm<kCopies>();
+    const int k = p >> 1;
+    const bool odd = p & 1, more = p + 1 < P;
+    // the limbs of an odd stage were asked for before the next weights
+    if (odd && more)
+      et_wait_vm<kPairCopies>();
     else
       et_wait_vm<0>();
     et_wait_lgkm0();
     et_barrier();
-    if (p + 2 < P) copy_stage(after, p + 2);
-    products(now, p);
-    unsigned char *const free = now;
-    now = next;
-    next = after;
-    after = free;
+    if (more) copy_limbs(a_mem + (~p & 1) * kA);
+    if (!odd && p + 2 < P) copy_pair(w_mem + (~k & 1) * kW, s_mem + (~k & 1) * kS, k + 1);
+    products(a_mem + (p & 1) * kA, w_mem + (k & 1) * kW, s_mem + (k & 1) * kS, p);
   }
 
   OT *y = static_cast<OT *>(a.Y);
@@ -369,13 +384,16 @@ hipError_t run_tile(const MoeExperts &p, hipStream_t stream) {
 
 template <typename XT, bool kSw>
 hipError_t run_tile_rows(const MoeExperts &p, hipStream_t stream) {
+  // Slots per tile by the mean of an expert (32 experts of 2 x 1024 x 4096, us
+  // with 32, 64 and 128 slots; bf16: mean 32 98, 97, 98; 48 101, 109, 113; 64
+  // 134, 110, 139; 96 166, 128, 140; 128 198, 171, 144.  fp16, whose FMAs grow
+  // with every slot: 128 198, 182, 175; 256 289, 301 with 64, 128.  fp32: 256
+  // 378, 598, one workgroup of 128 slots to a compute unit).
   const double mean = double(p.R) / double(std::max(1, std::min(p.R, p.E)));
-#ifdef ET_U
-  return run_tile<XT, kSw, ET_U>(p, stream);
-#endif
-  if (mean <= 32) return run_tile<XT, kSw, 2>(p, stream);
-  if (mean <= 96) return run_tile<XT, kSw, 4>(p, stream);
-  return run_tile<XT, kSw, 8>(p, stream);
+  if (mean <= 52) return run_tile<XT, kSw, 2>(p, stream);
+  if constexpr (sizeof(XT) == 4) return run_tile<XT, kSw, 4>(p, stream);
+  else if (mean <= (__is_same(XT, Bf16) ? 100 : 200)) return run_tile<XT, kSw, 4>(p, stream);
+  else return run_tile<XT, kSw, 8>(p, stream);
 }
 
 template <typename XT>
@@ -385,14 +403,18 @@ hipError_t run_tile_type(const MoeExperts &p, hipStream_t stream) {
 
 }  // namespace
 
-int experts_kernel(long R, long E) {
+// Mean slots per expert up to which the skinny kernel is the faster one (32
+// experts of 2 x 1024 x 4096, us skinny against the best tile: bf16 24 75, 87;
+// 32 87, 97; 48 119, 101; fp32 12 83, 84; 16 97, 92; 32 138, 109).
+int experts_kernel(long R, long E, int dtype) {
   const long active = std::max(1L, std::min(R, E));
-  return R >= 64 * active ? W4A16_EXPERTS_TILE : W4A16_EXPERTS_SKINNY;
+  return R > (dtype == W4A16_DTYPE_F32 ? 14 : 36) * active ? W4A16_EXPERTS_TILE
+                                                          : W4A16_EXPERTS_SKINNY;
 }
 
 size_t experts_workspace_bytes(long rows_x, long R, long E, int K, int dtype) {
   // the skinny kernel takes 16-bit activations as they are
-  if (experts_kernel(R, E) != W4A16_EXPERTS_TILE && dtype != W4A16_DTYPE_F32) return 0;
+  if (experts_kernel(R, E, dtype) != W4A16_EXPERTS_TILE && dtype != W4A16_DTYPE_F32) return 0;
   return limb_bytes(rows_x, K, dtype);
 }
 
@@ -405,7 +427,7 @@ hipError_t launch_experts_tile(const MoeExperts &p, hipStream_t stream) {
 }
 
 hipError_t launch_experts(const MoeExperts &p, hipStream_t stream) {
-  return experts_kernel(p.R, p.E) == W4A16_EXPERTS_TILE ? launch_experts_tile(p, stream)
+  return experts_kernel(p.R, p.E, p.dtype) == W4A16_EXPERTS_TILE ? launch_experts_tile(p, stream)
                                                        : launch_experts_skinny(p, stream);
 }
 

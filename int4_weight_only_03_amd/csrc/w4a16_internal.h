@@ -173,10 +173,9 @@ LimbLayout limb_layout(void *workspace, long rows, int K, int dtype);
 size_t limb_bytes(long rows, int K, int dtype);
 hipError_t launch_limbs(const MoeExperts &p, hipStream_t stream);
 // W4A16_EXPERTS_*: the kernel for a shape; its workspace
-int experts_kernel(long R, long E);
+int experts_kernel(long R, long E, int dtype);
 size_t experts_workspace_bytes(long rows_x, long R, long E, int K, int dtype);
 hipError_t launch_experts(const MoeExperts &p, hipStream_t stream);
-int experts_skinny_rows(long R, long E);
 hipError_t launch_experts_skinny(const MoeExperts &p, hipStream_t stream);
 hipError_t launch_experts_tile(const MoeExperts &p, hipStream_t stream);
 

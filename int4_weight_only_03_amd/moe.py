@@ -162,9 +162,9 @@ def w4a16_moe_route(logits, topk: int, bias=None, score="softmax", groups: int =
     return out
 
 
-def w4a16_experts_kernel(R: int, E: int) -> int:
+def w4a16_experts_kernel(R: int, E: int, dtype) -> int:
     """Kernel of the two products below for R slots over E experts (W4A16_EXPERTS_*)."""
-    return load().w4a16_experts_kernel(R, E)
+    return load().w4a16_experts_kernel(R, E, _code(dtype))
 
 
 def w4a16_grouped_swiglu_workspace_bytes(T: int, R: int, E: int, F: int, K: int, dtype) -> int:

@@ -53,8 +53,8 @@ def on(dev, *arrays):
     return [torch.from_numpy(np.ascontiguousarray(a)).to(dev) for a in arrays]
 
 
-def tile(R, E):
-    return pkg.w4a16_experts_kernel(R, E) == pkg.W4A16_EXPERTS_TILE
+def tile(R, E, dtype):
+    return pkg.w4a16_experts_kernel(R, E, TYPES[dtype]) == pkg.W4A16_EXPERTS_TILE
 
 
 def within(got, want, tol, what):
@@ -90,7 +90,7 @@ def run_swiglu(dev, counts, T, F, K, dtype, seed, spare=0):
     torch.cuda.synchronize()
     assert out is Hd
     assert torch.all(buf[:pad] == 77) and torch.all(buf[pad + len(tok) * F:] == 77)
-    H, tol = oracle.experts_swiglu(X, tok, off, qw, sc, dtype, tile(R, E))
+    H, tol = oracle.experts_swiglu(X, tok, off, qw, sc, dtype, tile(R, E, dtype))
     within(Hd[:len(tok)], H, tol, f"swiglu {dtype}")
     again = pkg.w4a16_gemm_grouped_swiglu(Xd, tokd, offd, qwd, scd)
     assert torch.equal(again[:len(tok)], Hd[:len(tok)])
@@ -101,11 +101,11 @@ SWIGLU = [
     ([1], 1, 1, 32, 0), ([0, 2, 0], 1, 33, 96, 0), ([1, 0, 0, 1], 1, 16, 128, 3),
     ([3, 1, 16, 17], 9, 70, 160, 0), ([15, 0, 33], 40, 45, 224, 5), ([8] * 8, 16, 64, 1056, 0),
     ([1] * 70, 5, 17, 64, 1), ([0] * 130 + [2] + [0] * 69, 3, 20, 256, 0),
-    # blocks of 32 and 64 slots, with rest blocks
+    # several items an expert, with rest items; from 15 (fp32) or 37 slots on tiles
     ([20, 33, 2], 25, 40, 288, 2), ([40, 64, 65, 1], 50, 50, 352, 0), ([63, 50], 99, 31, 96, 0),
     # the tile kernel: odd sizes, an odd number of groups, empty experts, rest tiles
     ([64, 0], 30, 64, 64, 64), ([128, 129, 1], 200, 65, 96, 0), ([300, 0, 5, 90], 111, 130, 160, 7),
-    ([512], 77, 1, 32, 0), ([200, 190], 400, 200, 544, 0),
+    ([512], 77, 1, 32, 0), ([200, 190], 400, 200, 544, 0), ([460, 210], 300, 150, 352, 0),
 ]
 
 
@@ -113,7 +113,7 @@ SWIGLU = [
 @pytest.mark.parametrize("counts,T,F,K,spare", SWIGLU)
 def test_swiglu_shapes(dev, counts, T, F, K, spare, dtype):
     E, R = len(counts), sum(counts) + spare
-    say("swiglu", counts[:8], T, F, K, dtype, "kernel", pkg.w4a16_experts_kernel(R, E))
+    say("swiglu", counts[:8], T, F, K, dtype, "tile", tile(R, E, dtype))
     run_swiglu(dev, counts, T, F, K, dtype, seed=R + F + K, spare=spare)
 
 
@@ -148,7 +148,7 @@ COMBINE = [
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("T,topk,E,N,K,live", COMBINE)
 def test_combine_shapes(dev, T, topk, E, N, K, live, dtype):
-    say("combine", T, topk, E, N, K, live, dtype, "kernel", pkg.w4a16_experts_kernel(T * topk, E))
+    say("combine", T, topk, E, N, K, live, dtype, "tile", tile(T * topk, E, dtype))
     rng = np.random.default_rng(T + N + K)
     Hd, Hv, off, qw, sc, slots, w = combine_case(dev, rng, T, topk, E, N, K, dtype, live)
     Hd[off[-1]:] = float("nan")  # rows of no expert are not used
@@ -158,7 +158,7 @@ def test_combine_shapes(dev, T, topk, E, N, K, live, dtype):
     Yd = pkg.w4a16_gemm_grouped_combine(Hd, *args, Y=buf[pad:pad + T * N].view(T, N))
     torch.cuda.synchronize()
     assert torch.all(buf[:pad] == 77) and torch.all(buf[pad + T * N:] == 77)
-    Y, tol = oracle.experts_combine(Hv, off, qw, sc, slots, w, dtype, tile(T * topk, E))
+    Y, tol = oracle.experts_combine(Hv, off, qw, sc, slots, w, dtype, tile(T * topk, E, dtype))
     within(Yd, Y, tol, f"combine {dtype}")
     assert torch.equal(pkg.w4a16_gemm_grouped_combine(Hd, *args), Yd)
 
@@ -196,7 +196,7 @@ def test_layer(dev, T, dtype):
         slots, tok, off = oracle.slot_lists(ids, E)
         assert np.array_equal(r.slots.cpu().numpy(), slots)
         m = off[-1]
-        big = tile(T * topk, E)
+        big = tile(T * topk, E, dtype)
         want, tol = oracle.experts_swiglu(x, tok[:m], off, gq, gs, dtype, big)
         within(H[:m], want, tol, "layer H")
         Hv = np.zeros((T * topk, F), np.float32)
@@ -277,7 +277,7 @@ def test_far_magnitudes(dev):
             tokd, offd, qwd, scd = on(dev, tok, off, qw, sc2)
             H = pkg.w4a16_gemm_grouped_swiglu(t.to(dev), tokd, offd, qwd, scd)
             want, tol = oracle.experts_swiglu(t.float().numpy(), tok, off, qw, sc2, dtype,
-                                              tile(2 * per, E))
+                                              tile(2 * per, E, dtype))
             within(H, want, tol, f"far {dtype} {per}")
 
 

@@ -120,9 +120,13 @@ def test_experts_workspaces(lib):
     assert f(0, 4, 8, 96, 64, torch.float16) == f(10, 0, 8, 96, 64, torch.float16) == 0
     g = pkg.w4a16_grouped_swiglu_workspace_bytes
     assert g(10, 40, 8, 96, 64, torch.bfloat16) == g(10, 40, 8, 96, 64, torch.float16) == 0
-    assert pkg.w4a16_experts_kernel(40, 8) == pkg.W4A16_EXPERTS_SKINNY
-    assert pkg.w4a16_experts_kernel(4096, 8) == pkg.W4A16_EXPERTS_TILE
-    assert pkg.w4a16_experts_kernel(0, 8) == pkg.w4a16_experts_kernel(8, 0) == 0
+    kernel = pkg.w4a16_experts_kernel
+    for dtype, most in ((torch.float32, 14), (torch.float16, 36), (torch.bfloat16, 36)):
+        assert kernel(8 * most, 8, dtype) == pkg.W4A16_EXPERTS_SKINNY
+        assert kernel(8 * most + 1, 8, dtype) == pkg.W4A16_EXPERTS_TILE
+        assert kernel(3, 8, dtype) == pkg.W4A16_EXPERTS_SKINNY
+        assert kernel(0, 8, dtype) == kernel(8, 0, dtype) == 0
+    assert binding.load().w4a16_experts_kernel(8, 8, 3) == 0
     # limbs of rows padded to 64 features (two for fp32), one factor per row
     assert g(64, 40, 8, 96, 96, torch.float32) == 64 * 128 * 4 + 64 * 4
     assert g(1024, 4096, 8, 96, 96, torch.bfloat16) == 1024 * 128 * 2 + 1024 * 4
