@@ -541,7 +541,7 @@ int w4a16_moe_route(const void *logits, const float *bias, const int32_t *num_to
                                   (made in the workspace) */
 
 /* The kernel for R slots over E experts (one of W4A16_EXPERTS_*): the tile past
- * 36 slots per expert (of the fewer of R and E), with fp32 activations past 14.
+ * 28 slots per expert (of the fewer of R and E), with fp32 activations past 10.
  * 0 for extents that are refused or a no-op, and for an unknown dtype.  Host
  * only. */
 int w4a16_experts_kernel(int64_t R, int64_t E, int32_t dtype);

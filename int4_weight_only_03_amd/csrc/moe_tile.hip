@@ -385,14 +385,15 @@ hipError_t run_tile(const MoeExperts &p, hipStream_t stream) {
 template <typename XT, bool kSw>
 hipError_t run_tile_rows(const MoeExperts &p, hipStream_t stream) {
   // Slots per tile by the mean of an expert (32 experts of 2 x 1024 x 4096, us
-  // with 32, 64 and 128 slots; bf16: mean 32 98, 97, 98; 48 101, 109, 113; 64
-  // 134, 110, 139; 96 166, 128, 140; 128 198, 171, 144.  fp16, whose FMAs grow
-  // with every slot: 128 198, 182, 175; 256 289, 301 with 64, 128.  fp32: 256
-  // 378, 598, one workgroup of 128 slots to a compute unit).
+  // with 32, 64 and 128 slots; bf16: mean 48 88, 98, 112; 56 109, 98, 123; 96
+  // 140, 118, 136; 128 164, 150, 137.  fp16, whose FMAs grow with every slot: 48
+  // 89, 110, 150; 256 279, 263, 292; 512 512, 455, 446.  fp32, with 32 and 64:
+  // 48 106, 138; 64 145, 139; 128 slots leave room for one workgroup only on a
+  // compute unit).
   const double mean = double(p.R) / double(std::max(1, std::min(p.R, p.E)));
   if (mean <= 52) return run_tile<XT, kSw, 2>(p, stream);
   if constexpr (sizeof(XT) == 4) return run_tile<XT, kSw, 4>(p, stream);
-  else if (mean <= (__is_same(XT, Bf16) ? 100 : 200)) return run_tile<XT, kSw, 4>(p, stream);
+  else if (mean <= (__is_same(XT, Bf16) ? 110 : 320)) return run_tile<XT, kSw, 4>(p, stream);
   else return run_tile<XT, kSw, 8>(p, stream);
 }
 
@@ -404,11 +405,11 @@ hipError_t run_tile_type(const MoeExperts &p, hipStream_t stream) {
 }  // namespace
 
 // Mean slots per expert up to which the skinny kernel is the faster one (32
-// experts of 2 x 1024 x 4096, us skinny against the best tile: bf16 24 75, 87;
-// 32 87, 97; 48 119, 101; fp32 12 83, 84; 16 97, 92; 32 138, 109).
+// experts of 2 x 1024 x 4096, us skinny against the best tile: bf16 24 73, 82;
+// 32 87, 85; 48 119, 88; fp32 8 69, 72; 12 83, 80; 24 111, 95).
 int experts_kernel(long R, long E, int dtype) {
   const long active = std::max(1L, std::min(R, E));
-  return R > (dtype == W4A16_DTYPE_F32 ? 14 : 36) * active ? W4A16_EXPERTS_TILE
+  return R > (dtype == W4A16_DTYPE_F32 ? 10 : 28) * active ? W4A16_EXPERTS_TILE
                                                           : W4A16_EXPERTS_SKINNY;
 }
 

@@ -101,7 +101,7 @@ SWIGLU = [
     ([1], 1, 1, 32, 0), ([0, 2, 0], 1, 33, 96, 0), ([1, 0, 0, 1], 1, 16, 128, 3),
     ([3, 1, 16, 17], 9, 70, 160, 0), ([15, 0, 33], 40, 45, 224, 5), ([8] * 8, 16, 64, 1056, 0),
     ([1] * 70, 5, 17, 64, 1), ([0] * 130 + [2] + [0] * 69, 3, 20, 256, 0),
-    # several items an expert, with rest items; from 15 (fp32) or 37 slots on tiles
+    # several items an expert, with rest items; from 11 (fp32) or 29 slots on tiles
     ([20, 33, 2], 25, 40, 288, 2), ([40, 64, 65, 1], 50, 50, 352, 0), ([63, 50], 99, 31, 96, 0),
     # the tile kernel: odd sizes, an odd number of groups, empty experts, rest tiles
     ([64, 0], 30, 64, 64, 64), ([128, 129, 1], 200, 65, 96, 0), ([300, 0, 5, 90], 111, 130, 160, 7),
