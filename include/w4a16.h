@@ -491,6 +491,7 @@ int w4a16_gemm_split_packed(const float *X, const void *packed, float *Y, int64_
 #define W4A16_ROUTE_MAX_EXPERTS 1024
 #define W4A16_ROUTE_MAX_TOPK 32
 #define W4A16_ROUTE_MAX_GROUPS 64
+#define W4A16_ROUTE_MAX_TOKENS ((int64_t)1 << 25)
 
 /* Workspace bytes of w4a16_moe_route (0 up to 16 tokens, or for extents it
  * refuses).  Host only. */
@@ -524,7 +525,7 @@ size_t w4a16_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t topk);
  * [1, groups], an unknown score, dtype or group_top, a scale that is not
  * finite, an output that overlaps an input or another output, or a missing,
  * misaligned (256 bytes), too small or overlapping workspace;
- * W4A16_ERR_SHAPE for E, topk or groups above W4A16_ROUTE_MAX_* or
+ * W4A16_ERR_SHAPE for E, topk, groups or T above W4A16_ROUTE_MAX_* or
  * T * topk >= 2^31; W4A16_ERR_ALIGN for pointers not aligned to their elements.
  */
 int w4a16_moe_route(const void *logits, const float *bias, const int32_t *num_tokens,
@@ -574,7 +575,8 @@ size_t w4a16_grouped_swiglu_workspace_bytes(int64_t T, int64_t R, int64_t E, int
  * workspace: w4a16_grouped_swiglu_workspace_bytes, 256-byte aligned; may be
  * NULL where that is 0.  R == 0 or F == 0 is a no-op; T == 0 with R > 0 is
  * W4A16_ERR_ARG; an unknown dtype is W4A16_ERR_ARG; X and qweight 16-byte
- * aligned, H to its elements; otherwise errors as w4a16_gemm_grouped with
+ * aligned, H to its elements; W4A16_ERR_SHAPE also for extents whose tiles
+ * would be 2^24 workgroups or more; otherwise errors as w4a16_gemm_grouped with
  * N = 2F.
  */
 int w4a16_gemm_grouped_swiglu(const void *X, const int32_t *token_index,

@@ -42,7 +42,8 @@ constexpr int64_t kMaxSlots = 0x7fffffff;
 
 int route_extents(int64_t T, int64_t E, int64_t topk) {
   if (T < 0 || E <= 0 || topk <= 0 || topk > E) return W4A16_ERR_ARG;
-  if (E > W4A16_ROUTE_MAX_EXPERTS || topk > W4A16_ROUTE_MAX_TOPK || T > kMaxSlots / topk)
+  if (E > W4A16_ROUTE_MAX_EXPERTS || topk > W4A16_ROUTE_MAX_TOPK ||
+      T > W4A16_ROUTE_MAX_TOKENS || T > kMaxSlots / topk)
     return W4A16_ERR_SHAPE;
   return W4A16_OK;
 }
@@ -57,8 +58,7 @@ int experts_extents(int64_t rows, int64_t R, int64_t E, int64_t N, int64_t K, in
   if (rows > W4A16_MAX_M || R > W4A16_MAX_M || E > 65535 || N > W4A16_MAX_N / 2 - 4 ||
       K > W4A16_MAX_K)
     return W4A16_ERR_SHAPE;
-  // every launch has at most 2^31 - 1 workgroups, the smallest tile 16 slots by
-  // 16 outputs
+  // tiles are counted in 32 bits
   const int64_t active = std::min(R, E);
   if (((R + 15 * active) / 16 + 1) * ((N + 15) / 16 + 1) > kMaxSlots / 2) return W4A16_ERR_SHAPE;
   return W4A16_OK;
@@ -68,7 +68,12 @@ size_t combine_rows_bytes(int64_t R, int64_t N) {
   return (size_t(R) * size_t((N + 3) / 4 * 4) * 4 + 255) / 256 * 256;
 }
 
-int status(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP; }
+// The launchers refuse a grid that the hardware cannot take as an invalid
+// configuration.
+int status(hipError_t e) {
+  if (e == hipErrorInvalidConfiguration) return W4A16_ERR_SHAPE;
+  return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP;
+}
 
 }  // namespace
 
@@ -247,7 +252,7 @@ int w4a16_gemm_grouped_combine(const void *H, const int32_t *expert_offsets,
   p.swiglu = false;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const hipError_t e = w4a16::launch_experts(p, s);
-  if (e != hipSuccess) return W4A16_ERR_HIP;
+  if (e != hipSuccess) return status(e);
   return status(w4a16::launch_combine(static_cast<const float *>(workspace), slots, weights, Y,
                                       int(T), int(topk), int(R), int(N), p.ldy, dtype, s));
 }

@@ -45,6 +45,9 @@ __device__ __forceinline__ void expert_slots(const int32_t *__restrict__ offsets
   r1 = min(max(offsets[e + 1], r0), R);
 }
 
+// A launch of 256 threads a workgroup has at most this many (2^32 threads).
+constexpr long kMaxBlocks = (1L << 24) - 8;
+
 struct ExpertItem {
   int e;      // expert, -1 behind the last item
   int row0;   // first slot of the item

@@ -43,53 +43,56 @@ __device__ __forceinline__ void read8(const Bf16 *p, float (&v)[8]) {
 
 constexpr int kPrepThreads = 256;
 
-// One row per workgroup.
+// A workgroup takes every gridDim.x-th row.
 template <typename XT>
 __global__ void __launch_bounds__(kPrepThreads)
 experts_limbs(const XT *__restrict__ X, _Float16 *__restrict__ limbs, float *__restrict__ factor,
               int rows, int K, int KP) {
   __shared__ float part[kPrepThreads / 64];
-  const long t = blockIdx.x;
   const int tid = threadIdx.x;
-  const XT *x = X + t * K;
-  int e = 0;
-  if constexpr (!__is_same(XT, _Float16)) {
-    float mx = 0.0f;
-    for (int k = 8 * tid; k < K; k += 8 * kPrepThreads) {
-      float v[8];
-      read8(x + k, v);
+  for (long t = blockIdx.x; t < rows; t += gridDim.x) {
+    const XT *x = X + t * K;
+    int e = 0;
+    if constexpr (!__is_same(XT, _Float16)) {
+      float mx = 0.0f;
+      for (int k = 8 * tid; k < K; k += 8 * kPrepThreads) {
+        float v[8];
+        read8(x + k, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]));
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]));
+      }
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
+      if ((tid & 63) == 0) part[tid >> 6] = mx;
+      __syncthreads();
+      mx = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+      e = std::min(row_exponent(mx), 149);  // 2^-149 is the least fp32 number
+      __syncthreads();  // before the next row's parts
     }
+    if (tid == 0) factor[t] = ldexpf(1.0f, -e);
+    _Float16 *hi = limbs + t * KP, *lo = hi + long(rows) * KP;
+    for (int k = 8 * tid; k < KP; k += 8 * kPrepThreads) {
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (k < K) read8(x + k, v);
+      half8_t h, l;
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
-    if ((tid & 63) == 0) part[tid >> 6] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-    e = std::min(row_exponent(mx), 126);  // 2^-e is a normal number
-  }
-  if (tid == 0) factor[t] = ldexpf(1.0f, -e);
-  _Float16 *hi = limbs + t * KP, *lo = hi + long(rows) * KP;
-  for (int k = 8 * tid; k < KP; k += 8 * kPrepThreads) {
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (k < K) read8(x + k, v);
-    half8_t h, l;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int j = (i >> 1) + 4 * (i & 1);  // x0 x4 x1 x5 x2 x6 x3 x7
-      const float s = ldexpf(v[j], e);
-      h[i] = _Float16(s);
-      l[i] = _Float16(s - float(h[i]));
+      for (int i = 0; i < 8; ++i) {
+        const int j = (i >> 1) + 4 * (i & 1);  // x0 x4 x1 x5 x2 x6 x3 x7
+        const float s = ldexpf(v[j], e);
+        h[i] = _Float16(s);
+        l[i] = _Float16(s - float(h[i]));
+      }
+      *reinterpret_cast<half8_t *>(hi + k) = h;
+      if constexpr (sizeof(XT) == 4) *reinterpret_cast<half8_t *>(lo + k) = l;
     }
-    *reinterpret_cast<half8_t *>(hi + k) = h;
-    if constexpr (sizeof(XT) == 4) *reinterpret_cast<half8_t *>(lo + k) = l;
   }
 }
 
 template <typename XT>
 hipError_t run_limbs(const MoeExperts &p, hipStream_t stream) {
   const LimbLayout at = limb_layout(p.workspace, p.rows_x, p.K, p.dtype);
-  hipLaunchKernelGGL(experts_limbs<XT>, dim3(unsigned(p.rows_x)), dim3(kPrepThreads), 0, stream,
+  hipLaunchKernelGGL(experts_limbs<XT>, dim3(unsigned(std::min(long(p.rows_x), kMaxBlocks))),
+                     dim3(kPrepThreads), 0, stream,
                      static_cast<const XT *>(p.X), at.limbs, at.factor, p.rows_x, p.K, at.KP);
   return hipGetLastError();
 }

@@ -326,7 +326,7 @@ hipError_t run_skinny(ExpertArgs a, hipStream_t stream) {
   a.tiles_n = (a.N + 16 * NO - 1) / (16 * NO);
   const long tiles = long(a.tiles_n) * max_items(a.R, a.E, 4 * MR);
   const long blocks = (tiles * KW + kEsWaves - 1) / kEsWaves;
-  if (blocks < 1 || blocks > 0x7fffffffL) return hipErrorInvalidValue;
+  if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((experts_skinny<XT, MR, NT, KW, P, kOcc, kSw>), dim3(unsigned(blocks)),
                      dim3(kEsThreads), 0, stream, a);
   return hipGetLastError();

@@ -334,19 +334,19 @@ __global__ void __launch_bounds__(kEtThreads, 2) experts_tile(TileArgs a) {
       const int slot = row0 + m;
       long row = slot;
       if (a.token_index) row = std::min(std::max(a.token_index[slot], 0), a.rows_x - 1);
-      const float f = a.factor[row] * (kFolded ? 1.0f / kFold : 1.0f);
+      const float f = a.factor[row], f0 = kFolded ? 1.0f / kFold : 1.0f;
       const long at = long(slot) * a.ldy;
       if constexpr (kSw) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int n = n0 + 32 * wave + 16 * t + c;
-          if (n < N) y[at + n] = from_f32<OT>(silu_mul(acc[u][t][r] * f, acc[u][t + 2][r] * f));
+          if (n < N) y[at + n] = from_f32<OT>(silu_mul(acc[u][t][r] * f0 * f, acc[u][t + 2][r] * f0 * f));
         }
       } else {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int n = n0 + 64 * wave + 16 * t + c;
-          if (n < N) y[at + n] = from_f32<OT>(acc[u][t][r] * f);
+          if (n < N) y[at + n] = from_f32<OT>(acc[u][t][r] * f0 * f);
         }
       }
     }
@@ -374,7 +374,7 @@ hipError_t run_tile(const MoeExperts &p, hipStream_t stream) {
   a.ldy = p.ldy;
   a.tiles_n = (p.N + (kSw ? 128 : 256) - 1) / (kSw ? 128 : 256);
   const long tiles = long(a.tiles_n) * max_items(p.R, p.E, 16 * U);
-  if (tiles < 1 || tiles > 0x7ffffff0L) return hipErrorInvalidValue;
+  if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
   const hipError_t e = launch_limbs(p, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((experts_tile<U, L, OT, kSw, __is_same(XT, Bf16)>),

@@ -29,7 +29,7 @@ def route(lib, **change):
 @pytest.mark.parametrize("change,want", [
     (dict(T=-1), ARG), (dict(E=0), ARG), (dict(topk=0), ARG), (dict(topk=65), ARG),
     (dict(E=1032), SHAPE), (dict(topk=33), SHAPE), (dict(T=1 << 30), SHAPE),
-    (dict(T=1 << 62), SHAPE),
+    (dict(T=1 << 62), SHAPE), (dict(T=(1 << 25) + 1, topk=1), SHAPE),
     (dict(score=2), ARG), (dict(dtype=3), ARG), (dict(dtype=-1), ARG), (dict(groups=0), ARG),
     (dict(groups=7), ARG), (dict(groups=128, E=256), SHAPE), (dict(group_limit=0), ARG),
     (dict(group_limit=9), ARG), (dict(group_top=0), ARG), (dict(group_top=3), ARG),
@@ -52,7 +52,7 @@ def test_route_workspace(lib):
     assert [f(T, 256, 8) for T in (0, 1, 16)] == [0, 0, 0]
     assert f(17, 256, 8) == 2 * 256 * 4             # counts of blocks of 16 tokens
     assert f(4097, 1000, 8) == 257 * 1000 * 4
-    assert f(100, 2000, 8) == f(100, 64, 65) == f(-1, 64, 8) == 0
+    assert f((1 << 25) + 1, 64, 8) == f(100, 2000, 8) == f(100, 64, 65) == f(-1, 64, 8) == 0
 
 
 def swiglu(lib, **change):
@@ -79,6 +79,8 @@ EXPERTS = [
     (dict(token_index=at(1) + 1), ALIGN),
     (dict(H=at(0) + 128), ARG), (dict(H=at(3)), ARG), (dict(H=at(4)), ARG), (dict(H=at(2)), ARG),
     (dict(H=at(1)), ARG),
+    # more workgroups than a launch takes
+    (dict(R=65535, E=65535, F=40000, K=32, qweight=at(100), scales=at(200), H=at(300)), SHAPE),
     # 128 slots per expert: the tile kernel's limbs
     (dict(R=1024), ARG), (dict(R=1024, ws=at(6), ws_bytes=10), ARG),
     (dict(R=1024, ws=at(6) + 16, ws_bytes=1 << 30), ARG),
