@@ -41,39 +41,46 @@ __device__ __forceinline__ void read8(const Bf16 *p, float (&v)[8]) {
   }
 }
 
-constexpr int kPrepThreads = 256;
-
-// A workgroup takes every gridDim.x-th row.
-template <typename XT>
-__global__ void __launch_bounds__(kPrepThreads)
+// A workgroup of NTHR threads takes every gridDim.x-th row.  A thread's first 8
+// values stay in registers between the two passes, the others are read again.
+template <typename XT, int NTHR>
+__global__ void __launch_bounds__(NTHR)
 experts_limbs(const XT *__restrict__ X, _Float16 *__restrict__ limbs, float *__restrict__ factor,
               int rows, int K, int KP) {
-  __shared__ float part[kPrepThreads / 64];
+  __shared__ float part[NTHR / 64];
   const int tid = threadIdx.x;
   for (long t = blockIdx.x; t < rows; t += gridDim.x) {
     const XT *x = X + t * K;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (8 * tid < K) read8(x + 8 * tid, v);
     int e = 0;
     if constexpr (!__is_same(XT, _Float16)) {
       float mx = 0.0f;
-      for (int k = 8 * tid; k < K; k += 8 * kPrepThreads) {
-        float v[8];
-        read8(x + k, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]));
+      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]));
+      for (int k = 8 * (tid + NTHR); k < K; k += 8 * NTHR) {
+        float u[8];
+        read8(x + k, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(u[i]));
       }
 #pragma unroll
       for (int d = 32; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
       if ((tid & 63) == 0) part[tid >> 6] = mx;
       __syncthreads();
-      mx = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+#pragma unroll
+      for (int i = 0; i < NTHR / 64; ++i) mx = fmaxf(mx, part[i]);
       e = std::min(row_exponent(mx), 149);  // 2^-149 is the least fp32 number
       __syncthreads();  // before the next row's parts
     }
     if (tid == 0) factor[t] = ldexpf(1.0f, -e);
     _Float16 *hi = limbs + t * KP, *lo = hi + long(rows) * KP;
-    for (int k = 8 * tid; k < KP; k += 8 * kPrepThreads) {
-      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (k < K) read8(x + k, v);
+    for (int k = 8 * tid; k < KP; k += 8 * NTHR) {
+      if (k >= 8 * NTHR) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        if (k < K) read8(x + k, v);
+      }
       half8_t h, l;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -88,13 +95,20 @@ experts_limbs(const XT *__restrict__ X, _Float16 *__restrict__ limbs, float *__r
   }
 }
 
-template <typename XT>
+template <typename XT, int NTHR>
 hipError_t run_limbs(const MoeExperts &p, hipStream_t stream) {
   const LimbLayout at = limb_layout(p.workspace, p.rows_x, p.K, p.dtype);
-  hipLaunchKernelGGL(experts_limbs<XT>, dim3(unsigned(std::min(long(p.rows_x), kMaxBlocks))),
-                     dim3(kPrepThreads), 0, stream,
+  const long grid = std::min(long(p.rows_x), (1L << 32) / NTHR - 8);
+  hipLaunchKernelGGL((experts_limbs<XT, NTHR>), dim3(unsigned(grid)), dim3(NTHR), 0, stream,
                      static_cast<const XT *>(p.X), at.limbs, at.factor, p.rows_x, p.K, at.KP);
   return hipGetLastError();
+}
+
+template <typename XT>
+hipError_t run_limbs_row(const MoeExperts &p, hipStream_t stream) {
+  // Threads by the row's length (fp32, us with 256 and 1024; 16 rows of 7168: 4.6,
+  // 3.7; 4096 rows of 7168: 48.6, 37.2, of 4096: 25.4, 26.4, of 2048: 11.6, 17.2).
+  return p.K > 4096 ? run_limbs<XT, 1024>(p, stream) : run_limbs<XT, 256>(p, stream);
 }
 
 }  // namespace
@@ -116,9 +130,9 @@ size_t limb_bytes(long rows, int K, int dtype) {
 
 hipError_t launch_limbs(const MoeExperts &p, hipStream_t stream) {
   switch (p.dtype) {
-    case W4A16_DTYPE_F32: return run_limbs<float>(p, stream);
-    case W4A16_DTYPE_F16: return run_limbs<_Float16>(p, stream);
-    default: return run_limbs<Bf16>(p, stream);
+    case W4A16_DTYPE_F32: return run_limbs_row<float>(p, stream);
+    case W4A16_DTYPE_F16: return run_limbs_row<_Float16>(p, stream);
+    default: return run_limbs_row<Bf16>(p, stream);
   }
 }
 

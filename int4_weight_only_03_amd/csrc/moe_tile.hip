@@ -92,6 +92,7 @@ struct TileArgs {
   const float *sc;
   void *Y;
   int rows_x, R, E, N, G, KP, ldy, tiles_n;
+  bool pairs;  // rows of Y begin and end at pairs of outputs (gate/up form)
 };
 
 // U: row tiles of 16 slots, L limbs, OT the output type (kSw: the activations'
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(kEtThreads, 2) experts_tile(TileArgs a) {
   constexpr int kRows = 16 * U, kLimb = kRows * 128;
   constexpr int kA = L * kLimb, kW = 16384, kS = 4096;
   __shared__ __align__(16) unsigned char et_mem[2 * (kA + kW + kS)];
+  __shared__ __align__(16) float et_factor[kRows];
   unsigned char *const a_mem = et_mem, *const w_mem = et_mem + 2 * kA,
                       *const s_mem = w_mem + 2 * kW;
   constexpr int kPairCopies = 8;            // weights and scales, of a wave
@@ -149,15 +151,17 @@ __global__ void __launch_bounds__(kEtThreads, 2) experts_tile(TileArgs a) {
               16 * ((lane & 7) ^ ((r >> 1) & 7));
   }
   const long plane = long(a.rows_x) * a.KP * 2;
-  // Row of W of row i of this wave's 64.  Gate/up form: 0..31 are gate rows of
-  // outputs n0 + 32 w .. +31, 32..63 the up rows of the same.  Rows past N read
-  // row N - 1.
+  // Row of W of row i of this wave's 64, dealt so that a lane's sums of a slot
+  // are neighbouring outputs: row 16 t + c is that of output 64 w + 4 c + t; in
+  // the gate/up form t = 0, 1 are the gate rows of outputs 32 w + 2 c + t, t = 2, 3
+  // the up rows of the same.  Rows past N read row N - 1.
   auto w_row = [&](int i) -> long {
+    const int t = i >> 4, at = i & 15;
     long n;
     if constexpr (kSw)
-      n = std::min(n0 + 32 * wave + (i & 31), N - 1) + ((i & 32) ? long(N) : 0);
+      n = std::min(n0 + 32 * wave + 2 * at + (t & 1), N - 1) + (t >= 2 ? long(N) : 0);
     else
-      n = std::min(n0 + 64 * wave + i, N - 1);
+      n = std::min(n0 + 64 * wave + 4 * at + t, N - 1);
     return n + long(it.e) * (kSw ? 2 * long(N) : long(N));
   };
   // Weight copies j = 0..3: lane i writes 16 B: row 16 j + i / 4, chunk i % 4.
@@ -309,6 +313,13 @@ __global__ void __launch_bounds__(kEtThreads, 2) experts_tile(TileArgs a) {
   // stage, whose weights' image is.
   copy_limbs(a_mem);
   copy_pair(w_mem, s_mem, 0);
+  // the rows' factors for the store, on their way with the first copies (read
+  // there row by row, they cost a tenth of a tile's time)
+  if (tid < kRows) {
+    long row = row0 + std::min(tid, rows - 1);
+    if (a.token_index) row = std::min(std::max(a.token_index[row], 0), a.rows_x - 1);
+    et_factor[tid] = a.factor[row];
+  }
   for (int p = 0; p < P; ++p) {
     const int k = p >> 1;
     const bool odd = p & 1, more = p + 1 < P;
@@ -325,31 +336,38 @@ __global__ void __launch_bounds__(kEtThreads, 2) experts_tile(TileArgs a) {
   }
 
   OT *y = static_cast<OT *>(a.Y);
+  constexpr float f0 = kFolded ? 1.0f / kFold : 1.0f;
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int u = 0; u < U; ++u) {
+    const floatx4 f = *reinterpret_cast<const floatx4 *>(et_factor + 16 * u + 4 * R);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int m = 16 * u + 4 * R + r;
       if (m >= rows) continue;
-      const int slot = row0 + m;
-      long row = slot;
-      if (a.token_index) row = std::min(std::max(a.token_index[slot], 0), a.rows_x - 1);
-      const float f = a.factor[row], f0 = kFolded ? 1.0f / kFold : 1.0f;
-      const long at = long(slot) * a.ldy;
+      const long at = long(row0 + m) * a.ldy;
       if constexpr (kSw) {
+        const int n = n0 + 32 * wave + 2 * c;
+        OT h[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int n = n0 + 32 * wave + 16 * t + c;
-          if (n < N) y[at + n] = from_f32<OT>(silu_mul(acc[u][t][r] * f0 * f, acc[u][t + 2][r] * f0 * f));
+        for (int t = 0; t < 2; ++t)
+          h[t] = from_f32<OT>(silu_mul(acc[u][t][r] * f0 * f[r], acc[u][t + 2][r] * f0 * f[r]));
+        if (a.pairs) {
+          struct alignas(2 * sizeof(OT)) Two {
+            OT v[2];
+          };
+          if (n < N) *reinterpret_cast<Two *>(y + at + n) = Two{{h[0], h[1]}};
+        } else {
+          if (n < N) y[at + n] = h[0];
+          if (n + 1 < N) y[at + n + 1] = h[1];
         }
       } else {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int n = n0 + 64 * wave + 16 * t + c;
-          if (n < N) y[at + n] = from_f32<OT>(acc[u][t][r] * f0 * f);
-        }
+        // rows of Y have room for a multiple of 4 outputs
+        const int n = n0 + 64 * wave + 4 * c;
+        const floatx4 d = {acc[u][0][r], acc[u][1][r], acc[u][2][r], acc[u][3][r]};
+        if (n < N) *reinterpret_cast<floatx4 *>(y + at + n) = d * f0 * f[r];
       }
     }
+  }
 }
 
 template <typename XT, bool kSw, int U>
@@ -372,6 +390,7 @@ hipError_t run_tile(const MoeExperts &p, hipStream_t stream) {
   a.N = p.N;
   a.G = p.K / kGroup;
   a.ldy = p.ldy;
+  a.pairs = p.N % 2 == 0 && reinterpret_cast<uintptr_t>(p.Y) % (2 * sizeof(OT)) == 0;
   a.tiles_n = (p.N + (kSw ? 128 : 256) - 1) / (kSw ? 128 : 256);
   const long tiles = long(a.tiles_n) * max_items(p.R, p.E, 16 * U);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
