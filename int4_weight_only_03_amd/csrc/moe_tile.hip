@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(kEtThreads, 2) experts_tile(TileArgs a) {
           b[t] = b[t] * half8_t{f, f, f, f, f, f, f, f};
         }
       }
+      if constexpr (kFolded) __builtin_amdgcn_s_setprio(2);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         half8_t x[L];
@@ -307,6 +308,12 @@ __global__ void __launch_bounds__(kEtThreads, 2) experts_tile(TileArgs a) {
     }
   };
 
+  // Folded weights: the wave that has come to its products goes first until the
+  // stage's end, while the other wave of its SIMD converts or copies (us without
+  // and with it, bf16, 32 experts: 2 x 2048 x 7168, mean 512: 1002, 967; 2 x 1024
+  // x 4096, mean 150: 134, 124; 688: 400, 373; but 325: 216, 229, a launch whose
+  // last tiles leave half the card empty.  fp16 and fp32 lose, 2 to 10 %).
+  //
   // At a stage's start its copies have landed in this wave; past the barrier
   // they have in every wave, and every wave is past the stage before, whose
   // limbs' image is then filled again, and past the two stages before an even
@@ -333,6 +340,7 @@ __global__ void __launch_bounds__(kEtThreads, 2) experts_tile(TileArgs a) {
     if (more) copy_limbs(a_mem + (~p & 1) * kA);
     if (!odd && p + 2 < P) copy_pair(w_mem + (~k & 1) * kW, s_mem + (~k & 1) * kS, k + 1);
     products(a_mem + (p & 1) * kA, w_mem + (k & 1) * kW, s_mem + (k & 1) * kS, p);
+    if constexpr (kFolded) __builtin_amdgcn_s_setprio(0);
   }
 
   OT *y = static_cast<OT *>(a.Y);
