@@ -32,15 +32,18 @@
 // of 16 stands in tile row 4 (i % 4) + i / 4, so that up to 4 MR slots fill only
 // the first MR of D's registers and the others cost no scale FMA.
 //
-// A wave takes 4 MR slots of one expert by NT x 16 rows of W (gate
-// tiles, then the up tiles of the same outputs) over blocks of 16 groups; KW
-// waves of a workgroup share a tile, taking blocks in turn, and their sums are
-// added in wave order in LDS.  The next block's weights fly while a block is
-// worked on.  Its scales come in one load per 16 rows of W and block (64 bytes
-// a row) and pass through the wave's own LDS words: loaded step by step, 16
-// bytes a row, they cost more than the weights (measured on 147 MB in this
-// pattern, loads alone: 22.4 us without scales, 34.8 with them step by step,
-// 27.9 by blocks).
+// A wave takes 4 MR slots of one expert by NT x 16 rows of W (gate tiles, then
+// the up tiles of the same outputs); KW waves of a workgroup share a tile and
+// its steps in turn, and their sums are added in wave order in LDS.  So the
+// waves read a row's next 64 bytes each at about the same time, and a cache line
+// that two steps share is fetched once (taking blocks of 4 steps in turn: 342 MB
+// fetched for 215 at 2080 features, whose rows end inside a line, and 61.7 us;
+// so 290 MB and 59.1 us with 2 waves, 212 MB and 56.0 us with 4).  The next
+// steps' weights fly while one is worked on.  The scales of a wave's 4 steps come
+// in one load per 16 rows of W (16 bytes a step and row) and pass through the
+// wave's own LDS words: loaded step by step they cost more than the weights
+// (measured on 147 MB in this pattern, loads alone: 22.4 us without scales, 34.8
+// with them step by step, 27.9 by blocks).
 
 #include "moe_common.h"
 #include "gemv_common.h"
@@ -127,8 +130,10 @@ __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a)
 #pragma unroll
     for (int r = 0; r < MR; ++r) acc[t][r] = 0.0f;
 
-  const int blocks = (G + kEsBlock - 1) / kEsBlock;
-  const int mine = it.e >= 0 && blocks > kw ? (blocks - kw + KW - 1) / KW : 0;
+  // The wave's j-th step of 4 groups; its steps come in blocks of 4.
+  auto step_of = [&](int j) { return j * KW + kw; };
+  const int steps = (G + 3) / 4, own = (steps - kw + KW - 1) / KW;
+  const int mine = it.e >= 0 ? (own + 3) / 4 : 0;
   if (mine > 0) {
     // The tile's first row of W and its scales (gate; the up rows are N
     // further), and this lane's row offsets from them (below 2^23 bytes).
@@ -158,21 +163,22 @@ __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a)
       XChunk<XT> x[4];
     };
     auto load = [&](Ops &o, int b, int j) {
-      const uint32_t gw = 16u * uint32_t(std::min(b * kEsBlock + 4 * j + R, G - 1));
+      const int g0 = 4 * step_of(4 * b + j);
+      const uint32_t gw = 16u * uint32_t(std::min(g0 + R, G - 1));
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         o.w[t] = *reinterpret_cast<const u32x4m *>(wbase + (t < NO ? 0 : up_w) + (woff[t % NO] + gw));
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const long g = 64 * long(std::min(b * kEsBlock + 4 * j + q, G - 1));
+        const long g = 64 * long(std::min(g0 + q, G - 1));
         o.x[q].v[0] = *reinterpret_cast<const u32x4m *>(xrow + g);
         if constexpr (kLimbs) o.x[q].v[1] = *reinterpret_cast<const u32x4m *>(xrow + plane + g);
       }
     };
-    // Scales of block b: lane l takes 4 groups of row l / 4 of each tile, the
-    // last shares moved back to end at G.
+    // Scales of block b: lane l takes those of step l % 4 for row l / 4 of each
+    // tile, shares that would pass G moved back to end there.
     auto load_s = [&](f32x4u (&s)[NT], int b) {
-      const uint32_t at = 4u * uint32_t(std::min(b * kEsBlock + 4 * (lane & 3), G - 4));
+      const uint32_t at = 4u * uint32_t(std::min(4 * step_of(4 * b + (lane & 3)), G - 4));
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         s[t] = *reinterpret_cast<const f32x4u *>(sbase + (t < NO ? 0 : up_s) + (soff[t % NO] + at));
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a)
     };
     auto keep_last = [&](const f32x4u (&s)[NT], int b) {
       const int g = 4 * (lane & 3);
-      const int moved = G >= 4 ? std::max(b * kEsBlock + g - (G - 4), 0) : 0;
+      const int moved = G >= 4 ? std::max(4 * step_of(4 * b + (lane & 3)) - (G - 4), 0) : 0;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -256,29 +262,28 @@ __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a)
     Ops ring[P];
     f32x4u s[NT];
     if (G >= 4)
-      load_s(s, kw);
+      load_s(s, 0);
     else
       load_few(s);
 #pragma unroll
-    for (int j = 0; j < P; ++j) load(ring[j], kw, j);
-    int b = kw;
-    for (int i = 1; i < mine; ++i) {  // every block but a wave's last is whole
+    for (int j = 0; j < P; ++j) load(ring[j], 0, j);
+    int b = 0;
+    for (; b + 1 < mine; ++b) {  // every block but a wave's last is whole
       keep_s(s);
-      load_s(s, b + KW);
+      load_s(s, b + 1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         process(ring[j % P], j, 4);
-        load(ring[j % P], j + P < 4 ? b : b + KW, (j + P) % 4);
+        load(ring[j % P], j + P < 4 ? b : b + 1, (j + P) % 4);
         __builtin_amdgcn_sched_barrier(0);
       }
-      b += KW;
     }
     keep_last(s, b);
-    const int rest = G - b * kEsBlock;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (4 * j >= rest) break;
-      process(ring[j % P], j, rest - 4 * j);
+      const int left = G - 4 * step_of(4 * b + j);
+      if (left <= 0) break;
+      process(ring[j % P], j, left);
       if (j + P < 4) load(ring[j % P], b, j + P);
     }
   }
@@ -345,12 +350,17 @@ hipError_t run_skinny_rows(const ExpertArgs &a, hipStream_t stream) {
 
 template <typename XT, bool kSw>
 hipError_t run_skinny_type(const ExpertArgs &a, hipStream_t stream) {
-  // Waves per tile: as many as there are blocks for up to 2, where few tiles
-  // leave the card to fill up to 4 (K = 7168, one token, 32 tiles: 15.8 against
-  // 24.5 us with 2; 512 tiles: 37.2 against 35.2).
+  // Waves per tile: as many as there are blocks for up to 2; up to 4 where few
+  // tiles leave the card to fill (K = 7168, one token, 32 tiles: 15.8 against
+  // 24.5 us with 2; 512 tiles: 37.2 against 35.2) and where rows of W are no whole
+  // 64 bytes, so that more waves share their lines (32 experts of 2 x 1024, us
+  // with 2 and 4: 16 tokens, top 4, K = 7200: bf16 72.5, 70.7, fp32 83.8, 81.2; 64
+  // tokens: 108, 93 and 130, 117; but K = 2080 in fp32 37.0, 38.3, and whole rows
+  // of 7168 60.7, 63.7 and 91.8, 85.4).
   const int blocks = (a.G + kEsBlock - 1) / kEsBlock;
   const long tiles = (long(a.N) + 31) / 32 * std::min(a.R, a.E);
-  if (blocks >= 4 && tiles < 512) return run_skinny_rows<XT, kSw, 4>(a, stream);
+  const bool ragged = a.G % 4 != 0 && blocks >= (sizeof(XT) == 4 ? 8 : 4);
+  if (ragged || (blocks >= 4 && tiles < 512)) return run_skinny_rows<XT, kSw, 4>(a, stream);
   if (blocks >= 2) return run_skinny_rows<XT, kSw, 2>(a, stream);
   return run_skinny_rows<XT, kSw, 1>(a, stream);
 }
