@@ -14,7 +14,7 @@ runs on.  Every call runs on its tensors' device, whichever is current.
 
 from __future__ import annotations
 
-import ctypes
+import contextlib
 from collections import namedtuple
 
 from .binding import GROUP, W4A16_OK, W4A16Error, load
@@ -61,43 +61,36 @@ def _tensor(t, dtype, name, device=None):
     return t
 
 
-class _Launch:
-    """The device and stream of one call.  Inside, the device is current and new
-    tensors belong to the stream."""
-
-    __slots__ = ("ptr", "_guard")
-
-    def __init__(self, device, stream):
-        import torch
-        if stream is None:
-            # the current stream's handle alone: a torch.cuda.Stream object of it
-            # takes 1.7 us more, as long as a small kernel
-            self.ptr = torch._C._cuda_getCurrentRawStream(device.index)
-            self._guard = None if torch.cuda.current_device() == device.index else \
-                torch.cuda.device(device)
-        else:
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self.ptr = stream.cuda_stream
-            self._guard = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+_HERE = contextlib.nullcontext()
 
 
-def _workspace(workspace, need, device):
-    if workspace is None and not need:
-        return None
+def _launch(device, stream):
+    """(stream handle, context) of one call: in the context the device is current and
+    new tensors belong to the stream."""
+    import torch
+    if stream is None:
+        # the current stream's handle alone: a torch.cuda.Stream object of it takes
+        # 1.7 us more, as long as a small kernel
+        here = torch.cuda.current_device() == device.index
+        return (torch._C._cuda_getCurrentRawStream(device.index),
+                _HERE if here else torch.cuda.device(device))
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _workspace(workspace, device, need, *extents):
+    """(tensor, address, bytes): the caller's, whose size the entry point checks, or a
+    new one of need(*extents) bytes"""
     import torch
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    return _tensor(workspace, torch.uint8, "workspace", device)
+        size = need(*extents)
+        if not size:
+            return None, None, 0
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    else:
+        _tensor(workspace, torch.uint8, "workspace", device)
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def _pointer(t):
@@ -142,10 +135,11 @@ def w4a16_moe_route(logits, topk: int, bias=None, score="softmax", groups: int =
     if num_tokens is not None and \
             _tensor(num_tokens, torch.int32, "num_tokens", device).numel() != 1:
         raise ValueError("num_tokens must have one element")
-    with _Launch(device, stream) as at:
+    at, context = _launch(device, stream)
+    with context:
         lib = load()
-        need = lib.w4a16_moe_route_workspace_bytes(T, E, topk)
-        ws = _workspace(workspace, need, device)
+        ws, ws_at, ws_bytes = _workspace(workspace, device, lib.w4a16_moe_route_workspace_bytes,
+                                         T, E, topk)
         if out is None:
             if topk < 1:
                 raise W4A16Error(1, "w4a16_moe_route")
@@ -162,7 +156,7 @@ def w4a16_moe_route(logits, topk: int, bias=None, score="softmax", groups: int =
             logits.data_ptr(), _pointer(bias), _pointer(num_tokens), out[0].data_ptr(),
             out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(), T, E,
             topk, _SCORES[score], groups, group_limit, group_top, int(bool(renormalize)), scale,
-            code, _pointer(ws), 0 if ws is None else ws.numel(), at.ptr)
+            code, ws_at, ws_bytes, at)
     if st != W4A16_OK:
         raise W4A16Error(st, "w4a16_moe_route")
     return out
@@ -210,18 +204,18 @@ def w4a16_gemm_grouped_swiglu(X, token_index, expert_offsets, qweight, scales, H
         raise ValueError("the gate/up weights need an even number of rows")
     F = rows // 2
     R = _tensor(token_index, torch.int32, "token_index", device).numel()
-    with _Launch(device, stream) as at:
+    at, context = _launch(device, stream)
+    with context:
         if H is None:
             H = torch.empty((R, F), dtype=X.dtype, device=device)
         elif tuple(_tensor(H, X.dtype, "H", device).shape) != (R, F):
             raise ValueError(f"H shape {tuple(H.shape)} != {(R, F)}")
         lib = load()
-        ws = _workspace(workspace,
-                        lib.w4a16_grouped_swiglu_workspace_bytes(T, R, E, F, K, code), device)
+        ws, ws_at, ws_bytes = _workspace(
+            workspace, device, lib.w4a16_grouped_swiglu_workspace_bytes, T, R, E, F, K, code)
         st = lib.w4a16_gemm_grouped_swiglu(
             X.data_ptr(), token_index.data_ptr(), expert_offsets.data_ptr(), qweight.data_ptr(),
-            scales.data_ptr(), H.data_ptr(), T, R, E, F, K, GROUP, code, _pointer(ws),
-            0 if ws is None else ws.numel(), at.ptr)
+            scales.data_ptr(), H.data_ptr(), T, R, E, F, K, GROUP, code, ws_at, ws_bytes, at)
     if st != W4A16_OK:
         raise W4A16Error(st, "w4a16_gemm_grouped_swiglu")
     return H
@@ -249,18 +243,19 @@ def w4a16_gemm_grouped_combine(H, expert_offsets, qweight, scales, slots, weight
     if R != T * topk:
         raise ValueError(f"H has {R} rows, the slots take {T * topk}")
     E, N = _experts(qweight, scales, expert_offsets, K, device)
-    with _Launch(device, stream) as at:
+    at, context = _launch(device, stream)
+    with context:
         if Y is None:
             Y = torch.empty((T, N), dtype=H.dtype, device=device)
         elif tuple(_tensor(Y, H.dtype, "Y", device).shape) != (T, N):
             raise ValueError(f"Y shape {tuple(Y.shape)} != {(T, N)}")
         lib = load()
-        ws = _workspace(workspace,
-                        lib.w4a16_grouped_combine_workspace_bytes(T, topk, E, N, K, code), device)
+        ws, ws_at, ws_bytes = _workspace(
+            workspace, device, lib.w4a16_grouped_combine_workspace_bytes, T, topk, E, N, K, code)
         st = lib.w4a16_gemm_grouped_combine(
             H.data_ptr(), expert_offsets.data_ptr(), qweight.data_ptr(), scales.data_ptr(),
             slots.data_ptr(), weights.data_ptr(), Y.data_ptr(), T, topk, E, N, K, GROUP, code,
-            _pointer(ws), 0 if ws is None else ws.numel(), at.ptr)
+            ws_at, ws_bytes, at)
     if st != W4A16_OK:
         raise W4A16Error(st, "w4a16_gemm_grouped_combine")
     return Y
