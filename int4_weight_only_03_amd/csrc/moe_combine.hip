@@ -4,7 +4,8 @@
 // of j in fp32 and rounded once.  Slots below 0 (places no expert took) add
 // nothing; a token without experts becomes 0.
 //
-// Bound by reading D.
+// Bound by reading D (16384 slots of 7168 columns into 4096 tokens: 104 us, 5.1
+// TB/s with what is written, a plain copy's rate).
 
 #include "moe_common.h"
 

@@ -32,8 +32,10 @@
 // is what takes the time), by 16 lanes, four tokens a wave, where they are many
 // (the same instructions serve four tokens).
 //
-// Bound: at few tokens by launch and the picks' latency; at many by VALU issue
-// of the selection.
+// Bound: at few tokens by launch and the picks' latency (one token of 256 experts
+// 6.3 us, 64 of 160 12.0); at many by VALU issue of the selection (16384 of 256
+// experts: 26 us to choose, 7 of them the few tokens' 64-bit keys at the end, and
+// 8 for the lists, where reading the logits takes 4).
 
 #include "moe_common.h"
 
@@ -663,10 +665,17 @@ __global__ void __launch_bounds__(kRtThreads) route_lists(RouteArgs a) {
     place_choices(a, t, min(64, t1 - t), a.ids + long(t) * a.topk, mask, before);
 }
 
-// Lanes per token: four tokens a wave past 16 tokens, while their experts,
-// choices and groups fit 16 lanes.
+// Lanes per token: 16 (four tokens a wave) past 16 tokens, while their experts,
+// choices and groups fit 16 lanes, but a whole wave for many experts and few
+// tokens, whose blocks of 16 tokens fit the card at once.  us with 64 and 16 lanes
+// (8 of E by sigmoid, bias and groups): E = 128, 64 tokens 13.8, 11.7, 4096 19.6,
+// 19.3, 8192 27.0, 20.3; E = 160, 64 tokens 13.9, 13.5, 1024 17.1, 17.7, 8192
+// 30.2, 23.7; E = 256, 64 tokens 14.0, 17.1, 4096 21.5, 25.7, 6000 29.3, 27.6,
+// 16384 50.8, 33.7.
 int lanes_per_token(long T, int E, int topk, int groups) {
-  return T > 16 && E <= 256 && topk <= 16 && groups <= 16 ? 16 : 64;
+  const bool fits = E <= 256 && topk <= 16 && groups <= 16;
+  const bool rather = E <= 128 || T > 256 * kRtWaves || (T <= 64 && E <= 192);
+  return T > 16 && fits && rather ? 16 : 64;
 }
 
 // blocks of the first kernel; one builds the lists as well

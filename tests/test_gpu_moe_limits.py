@@ -174,11 +174,17 @@ def lists_agree(r, E, topk):
     (70001, 4, 1, "fp32", dict(score="sigmoid")),
     (40000, 192, 6, "fp16", dict(groups=8, group_limit=3, group_top=2)),
     (17001, 256, 16, "bf16", dict(groups=16, group_limit=4)),
+    (4200, 250, 8, "fp32", dict(score="sigmoid", bias=0.1, groups=10, group_limit=4, group_top=2)),
+    (4200, 150, 8, "fp32", dict(bias=0.01)),
 ])
 def test_route_many_tokens(dev, T, E, topk, dtype, options):
     x = torch.randn(T, E, dtype=TYPES[dtype], device=dev)
     say("route", T, E, topk, dtype, options)
-    r = pkg.w4a16_moe_route(x, topk, **options)
+    bias = options.get("bias")
+    if bias is not None:
+        bias = bias * torch.randn(E, device=dev)
+    r = pkg.w4a16_moe_route(x, topk, **dict(options, bias=bias))
+    options = dict(options, bias=None if bias is None else bias.cpu().numpy())
     lists_agree(r, E, topk)
     for part in (slice(0, 200), slice(T // 2, T // 2 + 200), slice(T - 200, T)):
         ids, w = oracle.route(x[part].float().cpu().numpy(), topk, **options)
