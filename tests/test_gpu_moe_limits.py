@@ -238,3 +238,40 @@ def test_two_layers_at_once(dev):
         got = [layer(*i, stream=streams[j % 2]) for j, i in enumerate(inputs)]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_graphs_share_a_workspace(dev):
+    """Graphs of different batches on one workspace, replayed in turn with eager calls
+    on the same workspace between them."""
+    E, topk, F, K, N = 6, 2, 64, 160, 96
+    rng = np.random.default_rng(11)
+    gq, gs, dq, ds = on(dev, *weights_of(rng, E, 2 * F, K), *weights_of(rng, E, N, F))
+    batches = [(40, torch.float32), (9, torch.float32), (300, torch.bfloat16)]
+    need = max(max(pkg.w4a16_moe_route_workspace_bytes(T, E, topk),
+                   pkg.w4a16_grouped_swiglu_workspace_bytes(T, T * topk, E, F, K, t),
+                   pkg.w4a16_grouped_combine_workspace_bytes(T, topk, E, N, F, t))
+               for T, t in batches)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    inputs = [(torch.randn(T, E, device=dev), torch.randn(T, K, device=dev).to(t))
+              for T, t in batches]
+
+    def layer(logits, X):
+        r = pkg.w4a16_moe_route(logits, topk, workspace=ws)
+        H = pkg.w4a16_gemm_grouped_swiglu(X, r.token_index, r.expert_offsets, gq, gs, workspace=ws)
+        return pkg.w4a16_gemm_grouped_combine(H, r.expert_offsets, dq, ds, r.slots, r.weights,
+                                              workspace=ws)
+
+    graphs = []
+    for i in inputs:
+        layer(*i)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, layer(*i)))
+    for turn in range(3):
+        for (T, t), i, (g, out) in zip(batches, inputs, graphs):
+            i[0].copy_(torch.randn(T, E, device=dev))
+            i[1].copy_(torch.randn(T, K, device=dev))
+            out.zero_()
+            g.replay()
+            assert torch.equal(layer(*i), out)
