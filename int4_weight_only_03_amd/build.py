@@ -29,10 +29,7 @@ HOST_SOURCES = ["w4a16_api.cpp", "w4a16_io.cpp", "moe_api.cpp"]
 # FMAs read them directly, no accumulator-register copies); so do the tiled
 # kernel's block sums, which are added to running totals in VGPRs
 EXTRA = {"split.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         # the constants of the 64-bit exponential stay where they are used:
-         # hoisted out of the token loop they are spilled
-         "moe_route.hip": ["-mllvm", "-disable-machine-licm"]}
+         "tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def hipcc() -> str:

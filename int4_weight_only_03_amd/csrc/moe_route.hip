@@ -687,16 +687,21 @@ long choose_blocks(long T, int lanes) {
 template <int LP, int NV, bool kBias, bool kSigmoid>
 hipError_t run_route(const RouteArgs &a, hipStream_t stream) {
   const bool grouped = a.group_limit < a.groups;
-  if (LP == 64 && a.T == 1) {
-    hipLaunchKernelGGL((route_one<NV, kBias, kSigmoid>), dim3(1), dim3(64),
-                       grouped ? LP * NV * 8 : 0, stream, a);
-    return hipGetLastError();
+  if constexpr (LP == 64) {
+    if (a.T == 1) {
+      hipLaunchKernelGGL((route_one<NV, kBias, kSigmoid>), dim3(1), dim3(64),
+                         grouped ? LP * NV * 8 : 0, stream, a);
+      return hipGetLastError();
+    }
   }
   const int keys = grouped ? kRtThreads * NV : 0;
-  if (a.blocks == 1) {
-    hipLaunchKernelGGL((route_choose<LP, NV, kBias, kSigmoid, true>), dim3(1), dim3(kRtThreads),
-                       route_lds(a.E, keys, a.T * a.topk), stream, a);
-    return hipGetLastError();
+  // (past 192 experts 16 lanes have more than one block)
+  if constexpr (LP == 64 || NV < 16) {
+    if (a.blocks == 1) {
+      hipLaunchKernelGGL((route_choose<LP, NV, kBias, kSigmoid, true>), dim3(1), dim3(kRtThreads),
+                         route_lds(a.E, keys, a.T * a.topk), stream, a);
+      return hipGetLastError();
+    }
   }
   hipLaunchKernelGGL((route_choose<LP, NV, kBias, kSigmoid, false>), dim3(a.blocks),
                      dim3(kRtThreads), route_lds(a.E, keys, 0), stream, a);
