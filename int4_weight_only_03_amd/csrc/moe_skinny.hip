@@ -61,6 +61,8 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 constexpr int kEsWaves = 4;
 constexpr int kEsThreads = 64 * kEsWaves;
 constexpr int kEsBlock = 16;  // groups of a block: 4 steps of 4
+constexpr int NT = 4;         // tiles of 16 rows of W of a wave
+constexpr int P = 2;          // steps in flight of a wave
 
 // 8 activations x0..x7 in the order x0 x4 x1 x5 x2 x6 x3 x7 (that of the
 // nibble conversions)
@@ -103,10 +105,9 @@ __device__ __forceinline__ long row_of(const ExpertArgs &a, int slot) {
   return a.token_index ? std::min(std::max(a.token_index[slot], 0), a.rows_x - 1) : slot;
 }
 
-// kSw: W has 2N rows, Y is XT; else Y is fp32.  P: steps in flight per wave (2
-// or 4).  kOcc: waves per SIMD.
-template <typename XT, int MR, int NT, int KW, int P, int kOcc, bool kSw>
-__global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a) {
+// kSw: W has 2N rows, Y is XT; else Y is fp32.
+template <typename XT, int MR, int KW, bool kSw>
+__global__ void __launch_bounds__(kEsThreads, 2) experts_skinny(ExpertArgs a) {
   constexpr int NO = kSw ? NT / 2 : NT;
   constexpr int B = 4 * MR;  // slots of an item
   constexpr bool kLimbs = sizeof(XT) == 4;
@@ -326,14 +327,14 @@ __global__ void __launch_bounds__(kEsThreads, kOcc) experts_skinny(ExpertArgs a)
   }
 }
 
-template <typename XT, int MR, int NT, int KW, int P, int kOcc, bool kSw>
+template <typename XT, int MR, int KW, bool kSw>
 hipError_t run_skinny(ExpertArgs a, hipStream_t stream) {
   constexpr int NO = kSw ? NT / 2 : NT;
   a.tiles_n = (a.N + 16 * NO - 1) / (16 * NO);
   const long tiles = long(a.tiles_n) * max_items(a.R, a.E, 4 * MR);
   const long blocks = (tiles * KW + kEsWaves - 1) / kEsWaves;
   if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((experts_skinny<XT, MR, NT, KW, P, kOcc, kSw>), dim3(unsigned(blocks)),
+  hipLaunchKernelGGL((experts_skinny<XT, MR, KW, kSw>), dim3(unsigned(blocks)),
                      dim3(kEsThreads), 0, stream, a);
   return hipGetLastError();
 }
@@ -344,9 +345,9 @@ hipError_t run_skinny_rows(const ExpertArgs &a, hipStream_t stream) {
   // x 4096, mean 4: 47 us with 8, 41 with 16; with row tiles of 32 and 64
   // slots means of 12 to 24 took 72 to 91 us, with several items of 16 58 to 75)
   const double mean = double(a.R) / double(std::max(1, std::min(a.R, a.E)));
-  if (mean <= 1.25) return run_skinny<XT, 1, 4, KW, 2, 2, kSw>(a, stream);
-  if (mean <= 3.0) return run_skinny<XT, 2, 4, KW, 2, 2, kSw>(a, stream);
-  return run_skinny<XT, 4, 4, KW, 2, 2, kSw>(a, stream);
+  if (mean <= 1.25) return run_skinny<XT, 1, KW, kSw>(a, stream);
+  if (mean <= 3.0) return run_skinny<XT, 2, KW, kSw>(a, stream);
+  return run_skinny<XT, 4, KW, kSw>(a, stream);
 }
 
 template <typename XT, bool kSw>
