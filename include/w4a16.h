@@ -600,8 +600,8 @@ size_t w4a16_grouped_combine_workspace_bytes(int64_t T, int64_t topk, int64_t E,
  *   slots           int32 [T][topk]        below 0: no term (its weight is not used)
  *   weights         float [T][topk]
  *   Y               [T][N], dtype          0 for a token without a slot
- * The slots' products are kept in fp32 (in the workspace) and added in the
- * order of j.  Rows of H from expert_offsets[E] on are never used; a slot that
+ * The slots' products are kept in fp32 (in the workspace; for a single token
+ * mostly inside the one kernel that adds them) and added in the order of j.  Rows of H from expert_offsets[E] on are never used; a slot that
  * no expert owns gives an undefined row.  Slots past T*topk - 1 are clamped.
  * workspace: w4a16_grouped_combine_workspace_bytes, 256-byte aligned.
  * T == 0 or N == 0 is a no-op.  Otherwise as w4a16_gemm_grouped_swiglu.

@@ -251,6 +251,10 @@ int w4a16_gemm_grouped_combine(const void *H, const int32_t *expert_offsets,
   p.dtype = dtype;
   p.swiglu = false;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (w4a16::experts_token(long(T), long(topk), int(N), int(K), dtype)) {
+    p.Y = Y;
+    return status(w4a16::launch_experts_token(p, slots, weights, int(topk), s));
+  }
   const hipError_t e = w4a16::launch_experts(p, s);
   if (e != hipSuccess) return status(e);
   return status(w4a16::launch_combine(static_cast<const float *>(workspace), slots, weights, Y,

@@ -61,7 +61,7 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 constexpr int kEsWaves = 4;
 constexpr int kEsThreads = 64 * kEsWaves;
 constexpr int kEsBlock = 16;  // groups of a block: 4 steps of 4
-constexpr int NT = 4;         // tiles of 16 rows of W of a wave
+constexpr int kTokenWaves = 16;  // most waves of a workgroup of the one-token form
 constexpr int P = 2;          // steps in flight of a wave
 
 // 8 activations x0..x7 in the order x0 x4 x1 x5 x2 x6 x3 x7 (that of the
@@ -99,31 +99,65 @@ struct ExpertArgs {
   const float *sc;             // [E][N or 2N][G]
   void *Y;                     // [R][ldy]
   int rows_x, ldx, R, E, N, G, ldy, tiles_n;
+  // one-token form: Y[n] = sum_j weights[j] * D[slots[j]][n], in XT
+  const int32_t *slots;
+  const float *weights;
+  int topk;
 };
 
 __device__ __forceinline__ long row_of(const ExpertArgs &a, int slot) {
   return a.token_index ? std::min(std::max(a.token_index[slot], 0), a.rows_x - 1) : slot;
 }
 
+// The item of one slot, of whichever expert owns it (none: e = -1, as for a slot
+// below 0).  Every lane gets the same answer.
+__device__ __forceinline__ ExpertItem slot_item(const int32_t *__restrict__ offsets, int E, int R,
+                                                int slot) {
+  ExpertItem it = {-1, min(max(slot, 0), R - 1), 1, 0, 1, 1};
+  if (slot < 0) return it;
+  int owner = 0;  // experts that end before it
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + int(threadIdx.x & 63);
+    owner += __popcll(__ballot(e < E && offsets[min(e, E - 1) + 1] <= it.row0));
+  }
+  int r0 = 0, r1 = 0;
+  if (owner < E) expert_slots(offsets, owner, R, r0, r1);
+  if (it.row0 >= r0 && it.row0 < r1) it.e = owner;
+  return it;
+}
+
 // kSw: W has 2N rows, Y is XT; else Y is fp32.
-template <typename XT, int MR, int KW, bool kSw>
-__global__ void __launch_bounds__(kEsThreads, 2) experts_skinny(ExpertArgs a) {
+// kToken: the combination for a single token in the same launch.  KW waves a slot
+// and all of its slots make a workgroup, which adds them up in the order of the
+// choices and stores Y in XT.
+template <typename XT, int MR, int KW, bool kSw, bool kToken>
+__global__ void __launch_bounds__(kToken ? 64 * kTokenWaves : kEsThreads, kToken ? 4 : 2)
+experts_skinny(ExpertArgs a) {
+  static_assert(!kToken || (MR == 1 && !kSw), "one slot of a down projection");
+  constexpr int NT = kToken ? 2 : 4;  // tiles of 16 rows of W of a wave
   constexpr int NO = kSw ? NT / 2 : NT;
   constexpr int B = 4 * MR;  // slots of an item
   constexpr bool kLimbs = sizeof(XT) == 4;
   // per wave: a block's scales, row n of the tile at 64 n; at the end the sums
   constexpr int kTile = MR * NT * 64;
   constexpr int kWaveLds = KW > 1 && kTile > NT * 256 ? kTile : NT * 256;
-  __shared__ __align__(16) float es_lds[kEsWaves * kWaveLds];
+  __shared__ __align__(16) float es_lds[(kToken ? kTokenWaves : kEsWaves) * kWaveLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int c = lane & 15, R = lane >> 4;
   float *mem = es_lds + wave * kWaveLds;
   const int kw = KW > 1 ? wave % KW : 0;
-  const long tile = long(blockIdx.x) * (kEsWaves / KW) + wave / KW;
-  const int item = int(tile / a.tiles_n);
-  const int n0 = int(tile - long(item) * a.tiles_n) * 16 * NO;
-  const ExpertItem it = find_item(a.offsets, a.E, a.R, B, item);
+  int n0;
+  ExpertItem it;
+  if constexpr (kToken) {
+    n0 = int(blockIdx.x) * 16 * NO;
+    it = slot_item(a.offsets, a.E, a.R, a.slots[wave / KW]);
+  } else {
+    const long tile = long(blockIdx.x) * (kEsWaves / KW) + wave / KW;
+    const int item = int(tile / a.tiles_n);
+    n0 = int(tile - long(item) * a.tiles_n) * 16 * NO;
+    it = find_item(a.offsets, a.E, a.R, B, item);
+  }
   const int G = a.G, N = a.N;
 
   float acc[NT][MR];
@@ -290,6 +324,30 @@ __global__ void __launch_bounds__(kEsThreads, 2) experts_skinny(ExpertArgs a) {
     }
   }
 
+  if constexpr (kToken) {
+    // the slot stands in tile row 0: lanes 0..15 hold its outputs
+    __shared__ int es_there[kTokenWaves];
+    float f = 1.0f;
+    if constexpr (kLimbs) f = a.factor[it.row0];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (R == 0) mem[16 * t + c] = acc[t][0] * f;
+    if (lane == 0) es_there[wave] = it.e >= 0;
+    __syncthreads();
+    const int n = n0 + int(threadIdx.x);
+    if (threadIdx.x >= 16 * NT || n >= N) return;
+    float y = 0.0f;
+    for (int j = 0; j < a.topk; ++j) {
+      if (!es_there[j * KW]) continue;
+      const float *d = es_lds + j * KW * kWaveLds + threadIdx.x;
+      float sum = d[0];
+#pragma unroll
+      for (int k = 1; k < KW; ++k) sum += d[k * kWaveLds];
+      y = fmaf(a.weights[j], sum, y);
+    }
+    static_cast<XT *>(a.Y)[n] = from_f32<XT>(y);
+    return;
+  }
   if constexpr (KW > 1) {
     // sums of the tile's waves, in their order, on the first of them (each wave
     // is past its own words)
@@ -329,12 +387,12 @@ __global__ void __launch_bounds__(kEsThreads, 2) experts_skinny(ExpertArgs a) {
 
 template <typename XT, int MR, int KW, bool kSw>
 hipError_t run_skinny(ExpertArgs a, hipStream_t stream) {
-  constexpr int NO = kSw ? NT / 2 : NT;
+  constexpr int NO = kSw ? 2 : 4;
   a.tiles_n = (a.N + 16 * NO - 1) / (16 * NO);
   const long tiles = long(a.tiles_n) * max_items(a.R, a.E, 4 * MR);
   const long blocks = (tiles * KW + kEsWaves - 1) / kEsWaves;
   if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((experts_skinny<XT, MR, KW, kSw>), dim3(unsigned(blocks)),
+  hipLaunchKernelGGL((experts_skinny<XT, MR, KW, kSw, false>), dim3(unsigned(blocks)),
                      dim3(kEsThreads), 0, stream, a);
   return hipGetLastError();
 }
@@ -367,10 +425,26 @@ hipError_t run_skinny_type(const ExpertArgs &a, hipStream_t stream) {
   return run_skinny_rows<XT, kSw, 1>(a, stream);
 }
 
-}  // namespace
+template <typename XT>
+hipError_t run_token(const ExpertArgs &a, hipStream_t stream) {
+  // waves of a slot: what the workgroup has room for, while each has a block
+  const int blocks = (a.G + kEsBlock - 1) / kEsBlock;
+  const int kw = std::min(kTokenWaves / a.topk, blocks);
+  const dim3 grid(unsigned((a.N + 31) / 32));
+  if (kw >= 4)
+    hipLaunchKernelGGL((experts_skinny<XT, 1, 4, false, true>), grid, dim3(64 * 4 * a.topk), 0,
+                       stream, a);
+  else if (kw >= 2)
+    hipLaunchKernelGGL((experts_skinny<XT, 1, 2, false, true>), grid, dim3(64 * 2 * a.topk), 0,
+                       stream, a);
+  else
+    hipLaunchKernelGGL((experts_skinny<XT, 1, 1, false, true>), grid, dim3(64 * a.topk), 0, stream,
+                       a);
+  return hipGetLastError();
+}
 
-hipError_t launch_experts_skinny(const MoeExperts &p, hipStream_t stream) {
-  ExpertArgs a;
+// The arguments of a call; fp32 activations' limbs are made on the way.
+hipError_t prepare(const MoeExperts &p, ExpertArgs &a, hipStream_t stream) {
   a.X = p.X;
   a.ldx = p.K;
   a.factor = nullptr;
@@ -394,6 +468,46 @@ hipError_t launch_experts_skinny(const MoeExperts &p, hipStream_t stream) {
   a.G = p.K / kGroup;
   a.ldy = p.ldy;
   a.tiles_n = 0;
+  a.slots = nullptr;
+  a.weights = nullptr;
+  a.topk = 0;
+  return hipSuccess;
+}
+
+}  // namespace
+
+// Where the one-token form is the faster: a launch less (4.5 us), but a workgroup
+// has all of a column's slots to read, at 28 bytes a ns (20 with two limbs) where
+// the tiles of the general form share them out over the card, 4200 a ns (bf16, us
+// general against one-token: 8 slots of 7168 x 2048 22.2, 18.0; 4 of 7168 x 512
+// 9.8, 5.1; 8 of 2080 x 1408 13.1, 12.1, fp32 16.6, 18.2; 2 of 1024 x 4096 12.0,
+// 8.7, 4 of them 12.9, 15.1).
+bool experts_token(long T, long topk, int N, int K, int dtype) {
+  const long groups = (long(N) + 31) / 32;
+  if (T != 1 || topk > kTokenWaves || groups > kMaxBlocks / 4) return false;
+  const double bytes = 20.0 * K * topk;  // of a workgroup: 32 rows, 5/8 byte a weight
+  return bytes / (dtype == W4A16_DTYPE_F32 ? 20e3 : 28e3) <= 4.5 + groups * bytes / 4.2e6;
+}
+
+hipError_t launch_experts_token(const MoeExperts &p, const int32_t *slots, const float *weights,
+                                int topk, hipStream_t stream) {
+  ExpertArgs a;
+  const hipError_t e = prepare(p, a, stream);
+  if (e != hipSuccess) return e;
+  a.slots = slots;
+  a.weights = weights;
+  a.topk = topk;
+  switch (p.dtype) {
+    case W4A16_DTYPE_F32: return run_token<float>(a, stream);
+    case W4A16_DTYPE_F16: return run_token<_Float16>(a, stream);
+    default: return run_token<Bf16>(a, stream);
+  }
+}
+
+hipError_t launch_experts_skinny(const MoeExperts &p, hipStream_t stream) {
+  ExpertArgs a;
+  const hipError_t e = prepare(p, a, stream);
+  if (e != hipSuccess) return e;
   switch (p.dtype) {
     case W4A16_DTYPE_F32:
       return p.swiglu ? run_skinny_type<float, true>(a, stream)

@@ -178,6 +178,11 @@ size_t experts_workspace_bytes(long rows_x, long R, long E, int K, int dtype);
 hipError_t launch_experts(const MoeExperts &p, hipStream_t stream);
 hipError_t launch_experts_skinny(const MoeExperts &p, hipStream_t stream);
 hipError_t launch_experts_tile(const MoeExperts &p, hipStream_t stream);
+// One token's down projections and their combination in one launch, Y in dtype,
+// where experts_token(T, topk, N, K, dtype).
+bool experts_token(long T, long topk, int N, int K, int dtype);
+hipError_t launch_experts_token(const MoeExperts &p, const int32_t *slots, const float *weights,
+                                int topk, hipStream_t stream);
 
 // Y[t][n] = sum_j weights[t][j] * D[slots[t][j]][n], D fp32 [R][ldd], Y [T][N]
 // in dtype; slots below 0 add nothing.

@@ -275,3 +275,49 @@ def test_two_graphs_share_a_workspace(dev):
             out.zero_()
             g.replay()
             assert torch.equal(layer(*i), out)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("topk,E,N,K", [
+    # waves of a slot: 4, 2 and 1, and K of fewer blocks than waves
+    (1, 1, 1, 32), (1, 5, 33, 2080), (3, 9, 100, 2048), (4, 7, 31, 96), (8, 64, 65, 1056),
+    (8, 130, 7168, 512), (5, 40, 97, 544), (16, 20, 300, 160), (9, 9, 64, 608),
+    (17, 33, 70, 96),                      # more choices than a workgroup's waves
+    (4, 6, 40, 8192), (16, 16, 64, 4096),  # workgroups too few for so much to read
+])
+def test_combine_of_one_token(dev, topk, E, N, K, dtype):
+    """Slots in any order, one of them named twice, some without an expert."""
+    rng = np.random.default_rng(topk * N + K)
+    ids = rng.permutation(E)[:topk].astype(np.int32)[None]
+    slots, _, off = oracle.slot_lists(ids, E)
+    qw, sc = weights_of(rng, E, N, K)
+    x = rng.standard_normal((topk, K)).astype(np.float32)
+    X = torch.from_numpy(x).to(TYPES[dtype])
+    say("one token", topk, E, N, K, dtype)
+    for change in range(3):
+        s, w = slots.copy(), rng.standard_normal((1, topk)).astype(np.float32)
+        if change == 1:
+            s[0, -1] = s[0, 0]
+        elif change == 2:
+            s[0, ::2], w[0, ::2] = -1, np.nan
+        buf = torch.full((N + 128,), 77.0, dtype=TYPES[dtype], device=dev)
+        Y = pkg.w4a16_gemm_grouped_combine(X.to(dev), *on(dev, off, qw, sc, s, w),
+                                           Y=buf[64:64 + N].view(1, N))
+        want, tol = oracle.experts_combine(X.float().numpy(), off, qw, sc, s, w, dtype, False)
+        close(Y, want, tol, f"change {change}")
+        assert torch.all(buf[:64] == 77) and torch.all(buf[64 + N:] == 77)
+
+
+def test_malformed_lists_of_one_token_stay_in_bounds(dev):
+    E, topk, N, K = 4, 6, 70, 96
+    rng = np.random.default_rng(3)
+    qw, sc = on(dev, *weights_of(rng, E, N, K))
+    X = torch.randn(topk, K, device=dev).half()
+    w = torch.rand(1, topk, device=dev)
+    buf = torch.full((N + 128,), 77.0, dtype=torch.half, device=dev)
+    for off in ([-3, 99, 1, 4, 70], [9, 9, 9, 9, 9], [0, 0, 0, 0, 0], [6, 5, 4, 3, 2]):
+        slots = torch.tensor([[-9, 99, 5, 0, 2 ** 31 - 1, -2 ** 31]], dtype=torch.int32, device=dev)
+        pkg.w4a16_gemm_grouped_combine(X, torch.tensor(off, dtype=torch.int32, device=dev), qw, sc,
+                                       slots, w, Y=buf[64:64 + N].view(1, N))
+    torch.cuda.synchronize()
+    assert torch.all(buf[:64] == 77) and torch.all(buf[64 + N:] == 77)
