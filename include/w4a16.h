@@ -566,12 +566,12 @@ size_t w4a16_grouped_swiglu_workspace_bytes(int64_t T, int64_t R, int64_t E, int
  * The weights of an expert without slots are not read.  token_index and
  * expert_offsets are clamped into range on the device.  fp32 activations (two
  * fp16 limbs per row, as w4a16_gemm_split) meet the tolerance of w4a16_gemm on
- * both sums, and so do fp16 ones.  bf16 ones
- * meet it with scale * |x| * (q + 40) in place of |x * w| (the skinny kernel
- * multiplies by q + 16 and takes 24 off again in fp32); the tile kernel scales
- * them per row into fp16, exactly for values down to 2^-28 of their row's
- * largest, and takes the scales and weights in fp16's 11 bits (at most 2^-10 of
- * |x * w| more).  A row of X holding Inf or NaN gives non-finite values in its slots.
+ * both sums, and so do fp16 ones.  bf16 ones meet it with scale * |x| * (q + 40)
+ * in place of |x * w| (the skinny kernel multiplies by q + 16 and takes 24 off
+ * again in fp32); the tile kernel scales them per row into fp16, exactly for
+ * values down to 2^-28 of their row's largest, and takes the scales and weights
+ * in fp16's 11 bits (at most 2^-10 of |x * w| more).  A row of X holding Inf or
+ * NaN gives non-finite values in its slots.
  * workspace: w4a16_grouped_swiglu_workspace_bytes, 256-byte aligned; may be
  * NULL where that is 0.  R == 0 or F == 0 is a no-op; T == 0 with R > 0 is
  * W4A16_ERR_ARG; an unknown dtype is W4A16_ERR_ARG; X and qweight 16-byte
@@ -601,8 +601,9 @@ size_t w4a16_grouped_combine_workspace_bytes(int64_t T, int64_t topk, int64_t E,
  *   weights         float [T][topk]
  *   Y               [T][N], dtype          0 for a token without a slot
  * The slots' products are kept in fp32 (in the workspace; for a single token
- * mostly inside the one kernel that adds them) and added in the order of j.  Rows of H from expert_offsets[E] on are never used; a slot that
- * no expert owns gives an undefined row.  Slots past T*topk - 1 are clamped.
+ * mostly inside the one kernel that adds them) and added in the order of j.
+ * Rows of H from expert_offsets[E] on are never used; a slot that no expert owns
+ * gives an undefined row.  Slots past T*topk - 1 are clamped.
  * workspace: w4a16_grouped_combine_workspace_bytes, 256-byte aligned.
  * T == 0 or N == 0 is a no-op.  Otherwise as w4a16_gemm_grouped_swiglu.
  */

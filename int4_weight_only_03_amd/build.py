@@ -23,7 +23,8 @@ ARCH = "gfx950"
 
 DEVICE_SOURCES = ["gemv.hip", "gemv_mfma.hip", "tile.hip", "split.hip", "grouped.hip",
                   "small_packed.hip", "read_floor.hip", "skinny.hip", "tile_mx.hip",
-                  "moe_route.hip", "moe_limbs.hip", "moe_skinny.hip", "moe_tile.hip", "moe_combine.hip"]
+                  "moe_route.hip", "moe_limbs.hip", "moe_skinny.hip", "moe_tile.hip",
+                  "moe_combine.hip"]
 HOST_SOURCES = ["w4a16_api.cpp", "w4a16_io.cpp", "moe_api.cpp"]
 # per-source options: the split path's MFMA results stay in VGPRs (the scale
 # FMAs read them directly, no accumulator-register copies); so do the tiled
