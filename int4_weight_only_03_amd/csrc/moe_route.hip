@@ -179,17 +179,27 @@ __device__ __forceinline__ void merge_two(KT &m1, KT &m2) {
   m1 = o1 > m1 ? o1 : m1;
 }
 
-// Whether fp32 values of `n` scores each lie closer than their errors.  A score
-// is off by at most 5 * 2^-24: sigmoid by s (1 - s) |x| 2^-24 < 0.3 (the
-// exponent's rounding), 0.5 (exp2, 1 ulp of e s^2), 1 (the sum) and 2 (the
-// reciprocal, 1 ulp) of 2^-24 times s; softmax terms by 0.4 + 2, the products
-// and the reciprocal of their sum by 5, times scores that are below 1/2 where
-// two compete.  Each addition rounds once more, in proportion to the value.
+// What an fp32 score is off by: at most 5 * 2^-24.  Sigmoid: s (1 - s) |x| 2^-24 < 0.3
+// (the exponent's rounding), 0.5 (exp2, 1 ulp of e s^2), 1 (the sum) and 2 (the
+// reciprocal, 1 ulp) of 2^-24 times s.  Softmax: terms 0.4 + 2, the products and the
+// reciprocal of their sum 5 in proportion to s, which two scores share 1 of.  A bias
+// added rounds once more, by 2^-24 of the key.
+constexpr float kUnit = 0x1p-24f;
+
+// whether two fp32 keys lie closer than their errors (and the difference's rounding)
 template <typename KT>
-__device__ __forceinline__ bool too_close(KT hi, KT lo, int n) {
+__device__ __forceinline__ bool too_close(KT hi, KT lo) {
   if constexpr (sizeof(KT) == 8) return false;  // 64-bit keys decide as they are
   const float d = float(hi) - float(lo);
-  return !(d > float(n) * (12 * 0x1p-24f + 4 * 0x1p-24f * fmaxf(fabsf(float(hi)), fabsf(float(lo)))));
+  return !(d > 12 * kUnit + 4 * kUnit * fmaxf(fabsf(float(hi)), fabsf(float(lo))));
+}
+
+// What the sum of n keys of magnitudes `size` together is off by: 5 units and its
+// rounding for each, and the roundings of their sum and of adding this error to it.
+// The keys may cancel, so their sum says nothing of it (one expert favoured by 10^4
+// beside one disfavoured by as much: worth about 1, off by up to 10^-3).
+__device__ __forceinline__ float worth_error(int n, float size) {
+  return kUnit * (6.0f * float(n) + 3.0f * size);
 }
 
 // Rank of a group of value `value` among a token's: h runs over the groups, g is
@@ -334,8 +344,8 @@ __device__ __forceinline__ bool select_experts(const Select &a, int E, const flo
     if (LP == 64 && L > 32) merge_two<32>(m1, m2);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // before the room is written again
     __builtin_amdgcn_wave_barrier();
-    KT value = m1;
-    if (a.group_top == 2 && m2 > low) value += m2;
+    const bool two = a.group_top == 2 && m2 > low;
+    const KT value = two ? m1 + m2 : m1;
     int rank = 0;
     if constexpr (LP == 64) {
       for (int h = 0; h < a.groups; ++h) rank += above(read_lane(value, h * L), h, value, g);
@@ -344,10 +354,16 @@ __device__ __forceinline__ bool select_experts(const Select &a, int E, const flo
     }
     const bool open = g < a.groups && m1 > low, keep = open && rank < a.group_limit;
     const unsigned long long kept = __ballot(keep) >> ((threadIdx.x & 63) & ~(LP - 1));
-    if (scores) {  // the least of the kept against the largest of the others
-      const KT least = -token_max<LP>(keep ? -value : low);
-      const KT most = token_max<LP>(open && !keep ? value : low);
-      sure = !(most > low && too_close(least, most, a.group_top));
+    if constexpr (sizeof(KT) == 4) {
+      // The least that a kept group can be worth against the most that another can.
+      // A worth past fp32's range has an infinite error: a group kept above, or left
+      // below, everything is passed over (NaN), any other leaves the token unsure.
+      if (scores) {
+        const float error = worth_error(two ? 2 : 1, fabsf(m1) + (two ? fabsf(m2) : 0.0f));
+        const float least = -token_max<LP>(keep ? error - value : low);
+        const float most = token_max<LP>(open && !keep ? value + error : low);
+        sure = least > most;
+      }
     }
     // e / gs = (e * ceil(2^20 / gs)) >> 20 for e < 1024 (gs < 1024: two groups
     // at least)
@@ -366,7 +382,7 @@ __device__ __forceinline__ bool select_experts(const Select &a, int E, const flo
 #pragma unroll
     for (int r = 1; r < NV; ++r) m = larger(m, key[r]);
     m = token_max<LP>(m);
-    if (kBias && j > 0 && m > low && too_close(last, m, 1)) sure = false;
+    if (kBias && j > 0 && m > low && too_close(last, m)) sure = false;
     last = m;
     if (j == a.topk) break;
     int at = 0x7fffffff;  // the lowest expert that has it
