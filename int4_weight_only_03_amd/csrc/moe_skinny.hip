@@ -18,12 +18,16 @@
 //         codes q - 8 (every product exact in fp32); the row's power of two is
 //         undone at the store;
 //   fp16  the activations as they are and the exact codes q - 8;
-//   bf16  the activations as they are and q + 16, which two VALU instructions
-//         per pair of codes make: an instruction on a B of -24 throughout gives
-//         the accumulator that takes the offset out again.  The terms are up
-//         to 31 + 24 units of the scale instead of 8 and cancel, so the fp32
-//         sums lose up to 3 bits more (2^-21 beside an output rounded to
-//         2^-8); nothing is spent per activation.
+//   bf16  the activations as they are and (q + 16) 2^-12, which two VALU
+//         instructions per pair of codes make: an instruction on a B of -24 2^-12
+//         throughout gives the accumulator that takes the offset out again, and
+//         the store undoes 2^-12.  The terms are up to 31 + 24 units of the scale
+//         instead of 8 and cancel, so the fp32 sums lose up to 3 bits more (2^-21
+//         beside an output rounded to 2^-8); nothing is spent per activation.
+//         With the power of two no group's sum leaves fp32's range: 32 (31 + 24)
+//         2^-12 of bf16's largest number is less than half of it, and 2^-12 of its
+//         least, 2^-133, is a multiple of fp32's least.  (Without it activations
+//         from 3e35 on overflowed.)
 //
 // Mapping: lane (c, R) (c = lane % 16, R = lane / 16) loads the 16 bytes of
 // group 4 s + R of W row c (64 contiguous bytes of each of 16 rows per
@@ -73,13 +77,16 @@ __device__ __forceinline__ u32x4m interleave8(u32x4m a) {
                 __builtin_amdgcn_perm(a.w, a.y, 0x07060302u)};
 }
 
-// bf16 q + 16 of the 8 nibbles of w: dword p holds nibbles p and p + 4.  In
-// [16, 32) a bf16 has 3 bits behind the point, so a nibble stands at bits 3..6.
+constexpr float kBf16Scale = 4096.0f;  // what the bf16 form's codes are divided by
+
+// bf16 (q + 16) 2^-12 of the 8 nibbles of w: dword p holds nibbles p and p + 4.  A
+// bf16 has 7 bits behind the leading one, so a nibble stands at bits 3..6 of those of
+// 16 2^-12 = 0x3B80.
 __device__ __forceinline__ bf16x8 nibbles_to_bf16_16(uint32_t w) {
-  const uint32_t p0 = __builtin_amdgcn_bitop3_b32(w << 3, 0x00780078u, 0x41804180u, 0xEA);
-  const uint32_t p1 = __builtin_amdgcn_bitop3_b32(w >> 1, 0x00780078u, 0x41804180u, 0xEA);
-  const uint32_t p2 = __builtin_amdgcn_bitop3_b32(w >> 5, 0x00780078u, 0x41804180u, 0xEA);
-  const uint32_t p3 = __builtin_amdgcn_bitop3_b32(w >> 9, 0x00780078u, 0x41804180u, 0xEA);
+  const uint32_t p0 = __builtin_amdgcn_bitop3_b32(w << 3, 0x00780078u, 0x3B803B80u, 0xEA);
+  const uint32_t p1 = __builtin_amdgcn_bitop3_b32(w >> 1, 0x00780078u, 0x3B803B80u, 0xEA);
+  const uint32_t p2 = __builtin_amdgcn_bitop3_b32(w >> 5, 0x00780078u, 0x3B803B80u, 0xEA);
+  const uint32_t p3 = __builtin_amdgcn_bitop3_b32(w >> 9, 0x00780078u, 0x3B803B80u, 0xEA);
   return __builtin_bit_cast(bf16x8, u32x4m{p0, p1, p2, p3});
 }
 
@@ -138,6 +145,7 @@ experts_skinny(ExpertArgs a) {
   constexpr int NO = kSw ? NT / 2 : NT;
   constexpr int B = 4 * MR;  // slots of an item
   constexpr bool kLimbs = sizeof(XT) == 4;
+  constexpr float kOnce = __is_same(XT, Bf16) ? kBf16Scale : 1.0f;  // factor of the sums
   // per wave: a block's scales, row n of the tile at 64 n; at the end the sums
   constexpr int kTile = MR * NT * 64;
   constexpr int kWaveLds = KW > 1 && kTile > NT * 256 ? kTile : NT * 256;
@@ -255,7 +263,7 @@ experts_skinny(ExpertArgs a) {
       floatx4 d0 = zero;
       if constexpr (__is_same(XT, Bf16)) {
         const bf16x8 off = __builtin_bit_cast(
-            bf16x8, u32x4m{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u});  // -24
+            bf16x8, u32x4m{0xBBC0BBC0u, 0xBBC0BBC0u, 0xBBC0BBC0u, 0xBBC0BBC0u});  // -24 2^-12
         d0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xa), off, zero, 0, 0,
                                                      0);
       }
@@ -327,7 +335,7 @@ experts_skinny(ExpertArgs a) {
   if constexpr (kToken) {
     // the slot stands in tile row 0: lanes 0..15 hold its outputs
     __shared__ int es_there[kTokenWaves];
-    float f = 1.0f;
+    float f = kOnce;
     if constexpr (kLimbs) f = a.factor[it.row0];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -369,7 +377,7 @@ experts_skinny(ExpertArgs a) {
   for (int r = 0; r < MR; ++r) {
     const int m = R + 4 * r;
     if (m >= it.rows) continue;
-    float f = 1.0f;
+    float f = kOnce;
     if constexpr (kLimbs) f = a.factor[row_of(a, it.row0 + m)];
     const long y = long(it.row0 + m) * a.ldy;
 #pragma unroll
