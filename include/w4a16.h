@@ -565,8 +565,10 @@ size_t w4a16_grouped_swiglu_workspace_bytes(int64_t T, int64_t R, int64_t E, int
  *   H               [R][F], dtype
  * The weights of an expert without slots are not read.  token_index and
  * expert_offsets are clamped into range on the device.  fp32 activations (two
- * fp16 limbs per row, as w4a16_gemm_split) meet the tolerance of w4a16_gemm on
- * both sums, and so do fp16 ones.  bf16 ones meet it with scale * |x| * (q + 40)
+ * fp16 limbs with one power of two per row, as w4a16_gemm_split, the low limb
+ * x2^11: 22 significant bits down to 2^-28 of the row's largest, below that an
+ * absolute error under 2^-50 of it) meet the tolerance of w4a16_gemm on both sums
+ * for rows that span up to 2^30, and fp16 ones for every row.  bf16 ones meet it with scale * |x| * (q + 40)
  * in place of |x * w| (the skinny kernel multiplies by q + 16 and takes 24 off
  * again in fp32); the tile kernel scales them per row into fp16, exactly for
  * values down to 2^-28 of their row's largest, and takes the scales and weights

@@ -17,6 +17,9 @@ struct Bf16 {
 };
 typedef unsigned int u32x4m __attribute__((ext_vector_type(4)));
 
+// power of two that the low limb of an fp32 activation is carried with
+constexpr float kLowScale = 2048.0f;
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(_Float16 x) { return float(x); }
 __device__ __forceinline__ float to_f32(Bf16 x) { return __uint_as_float(uint32_t(x.v) << 16); }

@@ -4,9 +4,11 @@
 // A row is scaled by a power of two (its largest magnitude into [2^14, 2^15);
 // fp16 rows stay as they are) and kept as one limb (fp16, bf16: exact for every
 // value within 2^-28 of its row's largest) or two (fp32: hi = f16(x'), lo =
-// f16(x' - hi), 22 significant bits down to 2^-17 of the row's largest, below
-// that an absolute error under 2^-39 of it).  Each 8 values are stored in the
-// order of the nibble conversion, x0 x4 x1 x5 x2 x6 x3 x7.
+// f16((x' - hi) 2^11), 22 significant bits down to 2^-28 of the row's largest,
+// below that an absolute error under 2^-50 of it: without the 2^11 the low limb
+// would reach fp16's subnormals, 2^-39 of it, and rows that span 2^26 the end of
+// the tolerance).  Each 8 values are stored in the order of the nibble conversion,
+// x0 x4 x1 x5 x2 x6 x3 x7.
 //
 // Layout: limb plane l of row t at (l * rows + t) * KP fp16 values, KP = K
 // rounded up to 64 (zeros behind K), then one fp32 factor 2^-e per row.
@@ -87,7 +89,7 @@ experts_limbs(const XT *__restrict__ X, _Float16 *__restrict__ limbs, float *__r
         const int j = (i >> 1) + 4 * (i & 1);  // x0 x4 x1 x5 x2 x6 x3 x7
         const float s = ldexpf(v[j], e);
         h[i] = _Float16(s);
-        l[i] = _Float16(s - float(h[i]));
+        l[i] = _Float16((s - float(h[i])) * kLowScale);
       }
       *reinterpret_cast<half8_t *>(hi + k) = h;
       if constexpr (sizeof(XT) == 4) *reinterpret_cast<half8_t *>(lo + k) = l;

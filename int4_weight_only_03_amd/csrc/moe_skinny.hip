@@ -15,8 +15,8 @@
 // K: one group of 32), fp32 accumulation, one fp32 FMA per output and group
 // for the group's scale:
 //   fp32  two fp16 limbs of each activation, from moe_limbs.hip, and the exact
-//         codes q - 8 (every product exact in fp32); the row's power of two is
-//         undone at the store;
+//         codes q - 8 (every product exact in fp32); the low limb's sum takes its
+//         2^-11 with one FMA, the row's power of two is undone at the store;
 //   fp16  the activations as they are and the exact codes q - 8;
 //   bf16  the activations as they are and (q + 16) 2^-12, which two VALU
 //         instructions per pair of codes make: an instruction on a B of -24 2^-12
@@ -276,9 +276,12 @@ experts_skinny(ExpertArgs a) {
         } else {
           const half8_t b = nibbles_to_f16(o.w[t][q]);
           d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, xa), b, zero, 0, 0, 0);
-          if constexpr (kLimbs)
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                __builtin_bit_cast(half8_t, o.x[q].v[sizeof(XT) / 4]), b, d, 0, 0, 0);
+          if constexpr (kLimbs) {
+            const floatx4 low = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                __builtin_bit_cast(half8_t, o.x[q].v[sizeof(XT) / 4]), b, zero, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < MR; ++r) d[r] = fmaf(low[r], 1.0f / kLowScale, d[r]);
+          }
         }
         const float s = q == 0 ? sc[t].x : q == 1 ? sc[t].y : q == 2 ? sc[t].z : sc[t].w;
 #pragma unroll

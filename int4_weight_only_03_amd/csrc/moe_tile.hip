@@ -12,8 +12,9 @@
 // outputs, so that both sums of an output lie in one lane); each of its 4 waves
 // all of the slots by 64 of the rows, so that no weight is converted twice.
 // The weights:
-//   fp32, fp16  the exact codes q - 8, every product exact in fp32, one fp32
-//         FMA per output and group for the scale;
+//   fp32, fp16  the exact codes q - 8 (for fp32's low limbs times their 2^-11),
+//         every product exact in fp32, one fp32 FMA per output and group for the
+//         scale;
 //   bf16  (q - 8) * scale * 2^10 in fp16, the scale rounded to it and the
 //         product, so that the products of all groups add up inside the matrix
 //         instructions.  Those roundings, at most 2^-10 of a weight together and
@@ -277,13 +278,17 @@ __global__ void __launch_bounds__(kEtThreads, 2) experts_tile(TileArgs a) {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
         w[t] = *reinterpret_cast<const uint32_t *>(wimg + (cread[q] ^ 32 * h) + 1024 * t);
-      half8_t b[4];
+      half8_t b[4], low[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         b[t] = nibbles_to_f16(w[t]);
         if constexpr (kFolded) {
           const _Float16 f = _Float16(q == 0 ? s[t].x : s[t].y);
           b[t] = b[t] * half8_t{f, f, f, f, f, f, f, f};
+        }
+        if constexpr (L == 2) {  // the low limbs' codes, exact
+          const _Float16 f = _Float16(1.0f / kLowScale);
+          low[t] = b[t] * half8_t{f, f, f, f, f, f, f, f};
         }
       }
       if constexpr (kFolded) __builtin_amdgcn_s_setprio(2);
@@ -300,7 +305,7 @@ __global__ void __launch_bounds__(kEtThreads, 2) experts_tile(TileArgs a) {
           } else {
             floatx4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[0], b[t], zero, 0, 0, 0);
             if constexpr (L == 2)
-              d = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[L - 1], b[t], d, 0, 0, 0);
+              d = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[L - 1], low[t], d, 0, 0, 0);
             const float sq = q == 0 ? s[t].x : s[t].y;
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[u][t][r] = fmaf(sq, d[r], acc[u][t][r]);
