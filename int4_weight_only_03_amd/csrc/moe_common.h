@@ -60,6 +60,12 @@ struct ExpertItem {
   int total;  // items of the launch
 };
 
+// More items than any launch has workgroups for.  A lane's count stops there, so that
+// the counts of lists that overlap (malformed offsets, up to E / 2 times R slots) do
+// not pass 32 bits: an item would be looked for where there is none, and its first
+// slot lie out of range.
+constexpr int kMostItems = 1 << 24;
+
 // Item `item` of the list (expert, block of up to B of its slots), experts
 // ascending.  Every lane of a wave calls it with the same arguments and gets
 // the same answer.  Lane l counts the blocks of experts l*per .. l*per+per-1
@@ -75,7 +81,7 @@ __device__ __forceinline__ ExpertItem find_item(const int32_t *__restrict__ offs
     if (e < E) {
       int r0, r1;
       expert_slots(offsets, e, R, r0, r1);
-      mine += (r1 - r0 + B - 1) / B;
+      mine = min(mine + (r1 - r0 + B - 1) / B, kMostItems);
     }
   }
   int incl = mine;
