@@ -21,7 +21,9 @@
 //
 // Slots are sorted by expert, then token.  A block of tokens counts its
 // choices per expert; a second kernel sums the blocks before its own and ranks
-// each choice inside its block.  A token takes an expert at most once, so 64
+// each choice inside its block (past 2^14 tokens or so a small kernel between adds
+// the counts up, so that reading them does not grow with the square of the tokens).
+// A token takes an expert at most once, so 64
 // tokens' choices of an expert are one 64-bit mask, ORed together in LDS (any
 // order gives the same mask), and a choice's rank is a population count: no
 // result depends on the order of atomics.  One block of up to 64 tokens does
@@ -63,6 +65,7 @@ struct RouteArgs {
   float scale;
   int at_once, blocks;         // the first kernel's tokens per block, blocks
   int chunk;                   // the second's tokens per block (a multiple of 64)
+  int step;                    // blocks of the first that a row of counts it reads stands for
 };
 
 // row of the counts: a multiple of 4 experts
@@ -624,8 +627,39 @@ __global__ void __launch_bounds__(kRtThreads) route_choose(RouteArgs a) {
   }
 }
 
+// Block b: the counts of the first kernel's blocks that make the second's block b,
+// added up in place of the first of them.
+__global__ void __launch_bounds__(kRtThreads) route_sums(RouteArgs a) {
+  extern __shared__ __align__(16) unsigned char rt_lds[];
+  auto *total = reinterpret_cast<int *>(rt_lds);  // [row]
+  const int row = padded(a.E), tid = threadIdx.x;
+  const int first = int(blockIdx.x) * a.step, end = min(first + a.step, a.blocks);
+  if (tid < row) total[tid] = 0;
+  __syncthreads();
+  int width = 16;
+  while (4 * width < row) width <<= 1;
+  const int e = 4 * (tid & (width - 1));
+  if (e < row) {
+    int4 all = make_int4(0, 0, 0, 0);
+#pragma unroll 8
+    for (int k = first + tid / width; k < end; k += kRtThreads / width) {
+      const int4 c = *reinterpret_cast<const int4 *>(a.counts + long(k) * row + e);
+      all.x += c.x;
+      all.y += c.y;
+      all.z += c.z;
+      all.w += c.w;
+    }
+    atomicAdd(&total[e], all.x);
+    atomicAdd(&total[e + 1], all.y);
+    atomicAdd(&total[e + 2], all.z);
+    atomicAdd(&total[e + 3], all.w);
+  }
+  __syncthreads();
+  if (tid < row) a.counts[long(first) * row + tid] = total[tid];
+}
+
 // Block b: slots of tokens [b chunk, (b + 1) chunk) from the counts of the first
-// kernel's `blocks` blocks of at_once tokens.
+// kernel's `blocks` blocks of at_once tokens, a row of them in every `step`.
 __global__ void __launch_bounds__(kRtThreads) route_lists(RouteArgs a) {
   extern __shared__ __align__(16) unsigned char rt_lds[];
   const int row = padded(a.E);
@@ -634,7 +668,9 @@ __global__ void __launch_bounds__(kRtThreads) route_lists(RouteArgs a) {
   int *before = total + row + 1;                                // [row]
   int *part = before + row;                                     // [kRtWaves]
   const int tid = threadIdx.x;
-  const int first = int(blockIdx.x) * (a.chunk / a.at_once);  // block of its first token
+  // rows of counts, and the row of its first token
+  const int rows = (a.blocks + a.step - 1) / a.step;
+  const int first = int(blockIdx.x) * (a.chunk / a.at_once / a.step);
   if (tid < row) total[tid] = before[tid] = 0;
   __syncthreads();
   // four experts a thread side by side, the blocks dealt to the thread groups
@@ -646,8 +682,8 @@ __global__ void __launch_bounds__(kRtThreads) route_lists(RouteArgs a) {
     int4 all = make_int4(0, 0, 0, 0), mine = all;
     const int step = kRtThreads / width;
 #pragma unroll 8
-    for (int k = tid / width; k < a.blocks; k += step) {
-      const int4 c = *reinterpret_cast<const int4 *>(a.counts + long(k) * row + e);
+    for (int k = tid / width; k < rows; k += step) {
+      const int4 c = *reinterpret_cast<const int4 *>(a.counts + long(k) * a.step * row + e);
       const int own = k < first ? -1 : 0;
       all.x += c.x;
       all.y += c.y;
@@ -700,6 +736,14 @@ long choose_blocks(long T, int lanes) {
   return std::max((T + at_once - 1) / at_once, 1L);
 }
 
+// Whether the counts are added up by the second kernel's blocks first (per_list: the
+// first kernel's blocks in each; 1: they are not).  Each of up to 256 blocks reads all
+// the counts there are, which grow with the tokens and the experts; added up they are
+// 256 rows (bf16, us without and with the launch more: 32768 tokens of 64 experts, 2
+// blocks each, 18.0, 19.6; 65536, 4, 27.4, 27.1; of 256 59.2, 52.8; 32768 of 1000, 8
+// blocks each, 151, 67; 2^21 of 1000 11585, 3071).
+int counts_step(int per_list) { return per_list >= 4 ? per_list : 1; }
+
 template <int LP, int NV, bool kBias, bool kSigmoid>
 hipError_t run_route(const RouteArgs &a, hipStream_t stream) {
   const bool grouped = a.group_limit < a.groups;
@@ -723,9 +767,15 @@ hipError_t run_route(const RouteArgs &a, hipStream_t stream) {
                      dim3(kRtThreads), route_lds(a.E, keys, 0), stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  const unsigned lists = unsigned((a.T + a.chunk - 1) / a.chunk);
+  if (a.step > 1) {
+    hipLaunchKernelGGL(route_sums, dim3(lists), dim3(kRtThreads), size_t(padded(a.E)) * 4, stream,
+                       a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   const size_t lds = size_t(a.E) * 8 + (2 * size_t(padded(a.E)) + 1 + kRtWaves) * 4;
-  hipLaunchKernelGGL(route_lists, dim3((a.T + a.chunk - 1) / a.chunk), dim3(kRtThreads), lds,
-                     stream, a);
+  hipLaunchKernelGGL(route_lists, dim3(lists), dim3(kRtThreads), lds, stream, a);
   return hipGetLastError();
 }
 
@@ -783,6 +833,7 @@ hipError_t launch_route(const MoeRoute &r, void *workspace, hipStream_t stream) 
   a.at_once = kRtThreads / lanes;
   a.blocks = int(choose_blocks(r.T, lanes));
   a.chunk = int(64 * ((long(r.T) + 64L * kRtMaxBlocks - 1) / (64L * kRtMaxBlocks)));
+  a.step = counts_step(a.chunk / a.at_once);
   a.dtype = r.dtype;
   return run_route_size(a, stream);
 }
