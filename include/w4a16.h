@@ -470,7 +470,8 @@ int w4a16_gemm_split_packed(const float *X, const void *packed, float *Y, int64_
  * experts, the experts' gate/up projections with their SwiGLU epilogue, and
  * their down projections combined back into the tokens.  The activations are
  * fp32, fp16 or bf16 (W4A16_DTYPE_*); sums are fp32, and each 16-bit output is
- * rounded once.  A caller runs
+ * rounded once.  With bf16 activations and more than 52 slots per expert the
+ * weights are rounded to fp16, too (see w4a16_gemm_grouped_swiglu).  A caller runs
  *     w4a16_moe_route            logits -> ids, weights, slots, token_index,
  *                                          expert_offsets
  *     w4a16_gemm_grouped_swiglu  X -> H, one row per slot
@@ -571,8 +572,11 @@ size_t w4a16_grouped_swiglu_workspace_bytes(int64_t T, int64_t R, int64_t E, int
  * for rows that span up to 2^30, and fp16 ones for every row.  bf16 ones meet it with scale * |x| * (q + 40)
  * in place of |x * w| (the skinny kernel multiplies by q + 16 and takes 24 off
  * again in fp32); the tile kernel scales them per row into fp16, exactly for
- * values down to 2^-28 of their row's largest, and takes the scales and weights
- * in fp16's 11 bits (at most 2^-10 of |x * w| more).  A row of X holding Inf or
+ * values down to 2^-28 of their row's largest, with an absolute error under 2^-39
+ * of it below, and past 52 slots per expert takes the scales and weights in fp16's
+ * 11 bits: at most 2^-10 of |x * w| more, in the root mean square 2^-12
+ * sqrt(sum y_g^2 + sum (x * w)^2), y_g the sums of the groups, for scales spread
+ * over their binades (the stored result is rounded by 2^-8 of itself).  A row of X holding Inf or
  * NaN gives non-finite values in its slots.
  * workspace: w4a16_grouped_swiglu_workspace_bytes, 256-byte aligned; may be
  * NULL where that is 0.  R == 0 or F == 0 is a no-op; T == 0 with R > 0 is

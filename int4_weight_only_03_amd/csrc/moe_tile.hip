@@ -15,13 +15,18 @@
 //   fp32, fp16  the exact codes q - 8 (for fp32's low limbs times their 2^-11),
 //         every product exact in fp32, one fp32 FMA per output and group for the
 //         scale;
-//   bf16  (q - 8) * scale * 2^10 in fp16, the scale rounded to it and the
-//         product, so that the products of all groups add up inside the matrix
-//         instructions.  Those roundings, at most 2^-10 of a weight together and
-//         independent from group to group, move a sum by about 2^-12 of its
-//         size beside the 2^-8 that the stored result is rounded by (fp16's
-//         2^-11 leaves no such room), and save the FMAs, 256 VALU instructions
-//         of a wave's 400 per stage.  A scale outside [2^-20, 4) would leave
+//   bf16  the same with tiles of 32 slots.  Larger ones take (q - 8) * scale * 2^10 in
+//         fp16, the scale rounded to it and the product, so that the products of
+//         all groups add up inside the matrix instructions.  That saves the FMAs,
+//         256 VALU instructions of a wave's 400 per stage (us without and with it,
+//         32 experts of 2 x 1024 x 4096: mean 32 84, 84; 128 166, 121; 256 272, 220;
+//         512 418, 338; of 2 x 2048 x 7168, mean 512: 1257 to 1287, 1000).  The two
+//         roundings change a product by at most 2^-10 of it.  The scale's is common
+//         to a group, so a sum is off by up to 2^-10 sum |x w|; where scales are
+//         spread over their binades its root mean square is under 2^-12
+//         sqrt(sum of the groups' sums squared + sum (x w)^2) (0.78 measured at 32 to
+//         7168 features), beside the 2^-8 of the result that storing it rounds by.
+//         fp16's 2^-11 leaves no such room.  A scale outside [2^-20, 4) would leave
 //         fp16's range: its group counts as 0 there, and a stage with such a
 //         group adds its exact codes' products, scaled in fp32, by themselves.
 //
@@ -411,7 +416,7 @@ hipError_t run_tile(const MoeExperts &p, hipStream_t stream) {
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
   const hipError_t e = launch_limbs(p, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((experts_tile<U, L, OT, kSw, __is_same(XT, Bf16)>),
+  hipLaunchKernelGGL((experts_tile<U, L, OT, kSw, __is_same(XT, Bf16) && (U > 2)>),
                      dim3(unsigned((tiles + 7) / 8 * 8)), dim3(kEtThreads), 0, stream, a);
   return hipGetLastError();
 }
