@@ -1,6 +1,6 @@
 // Shared by the mixture-of-experts kernels (moe_route.hip, moe_skinny.hip,
-// moe_tile.hip, moe_combine.hip): loads and stores of the three activation
-// types and the assignment of workgroups to (expert, block of slots) items.
+// moe_tile.hip, moe_combine.hip): stores of the three activation types and the
+// assignment of workgroups to (expert, block of slots) items.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -19,10 +19,6 @@ typedef unsigned int u32x4m __attribute__((ext_vector_type(4)));
 
 // power of two that the low limb of an fp32 activation is carried with
 constexpr float kLowScale = 2048.0f;
-
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(_Float16 x) { return float(x); }
-__device__ __forceinline__ float to_f32(Bf16 x) { return __uint_as_float(uint32_t(x.v) << 16); }
 
 // fp32 to the activation type, to nearest even (one rounding per output)
 template <typename T>

@@ -6,10 +6,12 @@
 // Documentation Edit Marks the Completion of a Major Engineering Milestone",
 // section "The INT4 Milestone").
 //
-// Bound by reading the active experts' weights once (5/8 byte a weight; 147 MB
-// for one token of 8 experts of 2 x 2048 x 7168 in 33 us, 4.4 TB/s): the weights
-// and the activations go from memory straight to registers, P steps of 4 groups
-// ahead, and nothing waits at a barrier before the end.
+// Bound by reading the active experts' weights (5/8 byte a weight; 147 MB for one
+// token of 8 experts of 2 x 2048 x 7168 in 33 us, 4.4 TB/s, where the loads alone
+// take 28): the weights and the activations go from memory straight to registers,
+// P steps of 4 groups ahead, and nothing waits at a barrier before the end.  They
+// are read once for every 16 slots of an expert, so twice from 17 to the 28 slots
+// where the tile kernel takes over (the second time mostly from the caches).
 //
 // Arithmetic, on 16x16x32 matrix instructions (A: 16 slots, B: 16 rows of W,
 // K: one group of 32), fp32 accumulation, one fp32 FMA per output and group

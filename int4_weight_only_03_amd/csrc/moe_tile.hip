@@ -36,8 +36,9 @@
 // one barrier.  A wave copies the weights and scales of its own rows.  Copied
 // stage by stage, 32 and 8 bytes a row, their requests held up all others (32
 // experts of 2 x 2048 x 7168, 16384 slots in bf16: 1127 us; so 1034).  With the
-// steps since then 968 us, 0.99 PFLOP/s (limbs included), the matrix units busy
-// half of the time: bound by their issue together with the conversion's.
+// steps since then 990 us, 0.97 PFLOP/s (limbs included; 1068 under the profiler's
+// trace), the matrix units busy half of the time: bound by their issue together
+// with the conversion's.
 //
 // Tiles are dealt so that each XCD works a contiguous run of them (the
 // hardware deals workgroups round-robin over the 8 XCDs), row blocks of an
