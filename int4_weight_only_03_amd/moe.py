@@ -130,6 +130,8 @@ def w4a16_moe_route(logits, topk: int, bias=None, score="softmax", groups: int =
     T, E = logits.shape
     if score not in _SCORES:
         raise ValueError(f"unknown score {score!r}")
+    if not 1 <= topk <= E:  # W4A16_ERR_ARG, before buffers are made for it
+        raise W4A16Error(1, "w4a16_moe_route")
     if bias is not None and tuple(_tensor(bias, torch.float32, "bias", device).shape) != (E,):
         raise ValueError(f"bias shape {tuple(bias.shape)} != {(E,)}")
     if num_tokens is not None and \
@@ -141,8 +143,6 @@ def w4a16_moe_route(logits, topk: int, bias=None, score="softmax", groups: int =
         ws, ws_at, ws_bytes = _workspace(workspace, device, lib.w4a16_moe_route_workspace_bytes,
                                          T, E, topk)
         if out is None:
-            if topk < 1:
-                raise W4A16Error(1, "w4a16_moe_route")
             out = w4a16_moe_routing(T, E, topk, device)
         else:
             each = (T, topk)
