@@ -565,19 +565,22 @@ size_t w4a16_grouped_swiglu_workspace_bytes(int64_t T, int64_t R, int64_t E, int
  *   qweight         int32 [E][2F][K/8], scales float [E][2F][K/32]
  *   H               [R][F], dtype
  * The weights of an expert without slots are not read.  token_index and
- * expert_offsets are clamped into range on the device.  fp32 activations (two
- * fp16 limbs with one power of two per row, as w4a16_gemm_split, the low limb
- * x2^11: 22 significant bits down to 2^-28 of the row's largest, below that an
- * absolute error under 2^-50 of it) meet the tolerance of w4a16_gemm on both sums
- * for rows that span up to 2^30, and fp16 ones for every row.  bf16 ones meet it with scale * |x| * (q + 40)
- * in place of |x * w| (the skinny kernel multiplies by q + 16 and takes 24 off
- * again in fp32); the tile kernel scales them per row into fp16, exactly for
- * values down to 2^-28 of their row's largest, with an absolute error under 2^-39
- * of it below, and past 52 slots per expert takes the scales and weights in fp16's
- * 11 bits: at most 2^-10 of |x * w| more, in the root mean square 2^-12
- * sqrt(sum y_g^2 + sum (x * w)^2), y_g the sums of the groups, for scales spread
- * over their binades (the stored result is rounded by 2^-8 of itself).  A row of X holding Inf or
- * NaN gives non-finite values in its slots.
+ * expert_offsets are clamped into range on the device.
+ * Accuracy of both sums, in the tolerance of w4a16_gemm:
+ *   fp32  two fp16 limbs with one power of two per row, as w4a16_gemm_split, the
+ *         low limb x2^11: 22 significant bits down to 2^-28 of the row's largest,
+ *         below that an absolute error under 2^-50 of it.  The tolerance holds for
+ *         rows that span up to 2^30.
+ *   fp16  the tolerance holds for every row.
+ *   bf16  the skinny kernel multiplies by q + 16 and takes 24 off again in fp32: it
+ *         holds with scale * |x| * (q + 40) in place of |x * w|.  The tile kernel
+ *         scales rows into fp16, exactly for values down to 2^-28 of their row's
+ *         largest, with an absolute error under 2^-39 of it below.  Past 52 slots
+ *         per expert (of the fewer of R and E) it also takes the scales and weights
+ *         in fp16's 11 bits: at most 2^-10 of |x * w| more, in the root mean square
+ *         2^-12 sqrt(sum y_g^2 + sum (x * w)^2), y_g the groups' sums, for scales
+ *         spread over their binades; storing rounds by 2^-8 of the result.
+ * A row of X holding Inf or NaN gives non-finite values in its slots.
  * workspace: w4a16_grouped_swiglu_workspace_bytes, 256-byte aligned; may be
  * NULL where that is 0.  R == 0 or F == 0 is a no-op; T == 0 with R > 0 is
  * W4A16_ERR_ARG; an unknown dtype is W4A16_ERR_ARG; X and qweight 16-byte
