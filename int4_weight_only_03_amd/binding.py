@@ -17,6 +17,7 @@ import numpy as np
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libw4a16.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "w4a16.h")
+HEADER_W8A8 = os.path.join(os.path.dirname(PKG), "include", "w8a8.h")
 
 GROUP = 32
 W4A16_OK = 0
@@ -111,12 +112,27 @@ _SIGS = {
                               ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
 }
 
+# include/w8a8.h
+_SIGS_W8A8 = {
+    "w8a8_quantize_weights": ([ctypes.c_void_p] * 3 + [ctypes.c_int64] * 2 + [ctypes.c_int32],
+                              ctypes.c_int),
+    "w8a8_quantize": ([ctypes.c_void_p] * 4 + [ctypes.c_int64] * 2 + [ctypes.c_int32] * 2 +
+                      [ctypes.c_void_p], ctypes.c_int),
+    "w8a8_rms_norm": ([ctypes.c_void_p] * 7 + [ctypes.c_int64] * 2 + [ctypes.c_float] +
+                      [ctypes.c_int32] * 2 + [ctypes.c_void_p], ctypes.c_int),
+    "w8a8_gemm": ([ctypes.c_void_p] * 5 + [ctypes.c_int64] * 3 + [ctypes.c_int32] * 2 +
+                  [ctypes.c_void_p], ctypes.c_int),
+    "w8a8_gemm_grouped": ([ctypes.c_void_p] * 7 + [ctypes.c_int64] * 5 + [ctypes.c_int32] * 2 +
+                          [ctypes.c_void_p], ctypes.c_int),
+    "w8a8_kernel": ([ctypes.c_int64] * 4 + [ctypes.c_int32], ctypes.c_int),
+}
 
-def header_functions() -> list[str]:
-    """Names of the functions include/w4a16.h declares."""
-    text = open(HEADER).read()
+
+def header_functions(header: str = HEADER, prefix: str = "w4a16") -> list[str]:
+    """Names of the functions a header (include/w4a16.h) declares."""
+    text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(w4a16_\w+)\s*\(", text)))
+    return sorted(set(re.findall(rf"\b({prefix}_\w+)\s*\(", text)))
 
 
 def load(path: str | None = None):
@@ -137,7 +153,7 @@ def load(path: str | None = None):
         from . import build as _build
         _build.build()
     lib = ctypes.CDLL(p)
-    for name, (args, res) in _SIGS.items():
+    for name, (args, res) in {**_SIGS, **_SIGS_W8A8}.items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res

@@ -44,3 +44,4 @@ from .moe_ref import (  # noqa: F401,E402
     route,
     slot_lists,
 )
+from . import w8a8_ref as w8a8  # noqa: F401,E402

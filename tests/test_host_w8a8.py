@@ -1,0 +1,185 @@
+"""Host side of the 8-bit operators (no GPU is touched): refusals of the C entry points,
+on device addresses that are never dereferenced, the weights' quantizer, the binding."""
+
+import numpy as np
+import pytest
+
+import oracle
+from int4_weight_only_03_amd import binding
+import int4_weight_only_03_amd as pkg
+
+OK, ARG, SHAPE, ALIGN, NONFINITE = 0, 1, 2, 3, 4
+GB = 1 << 30
+BIG = (1 << 30) + 1
+
+
+def at(i):
+    return (1 << 40) + i * 64 * GB
+
+
+def test_header_names_match_binding(lib):
+    names = set(binding.header_functions(binding.HEADER_W8A8, "w8a8"))
+    assert names == set(binding._SIGS_W8A8)
+    for name in names:
+        assert hasattr(lib, name) and hasattr(pkg, name)
+
+
+def quantize(lib, **change):
+    a = dict(X=at(0), num_rows=None, codes=at(1), scales=at(2), M=4, K=256, swiglu=0, dtype=0)
+    a.update(change)
+    return lib.w8a8_quantize(*a.values(), None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(M=0), OK), (dict(M=0, X=None, codes=None, scales=None), OK),
+    (dict(M=-1), ARG), (dict(K=0), ARG), (dict(K=-16), ARG), (dict(dtype=3), ARG),
+    (dict(dtype=-1), ARG), (dict(X=None), ARG), (dict(codes=None), ARG), (dict(scales=None), ARG),
+    (dict(codes=at(0)), ARG), (dict(scales=at(0) + 4 * 4 * 256 - 4), ARG),
+    (dict(X=at(0), codes=at(0) + 4 * 4 * 512 - 16, swiglu=1), ARG),
+    (dict(scales=at(1) + 16), ARG), (dict(num_rows=at(1)), ARG), (dict(num_rows=at(2)), ARG),
+    (dict(K=8), SHAPE), (dict(K=200), SHAPE), (dict(K=(1 << 17) + 16), SHAPE),
+    (dict(M=BIG), SHAPE), (dict(X=at(0) + 8), ALIGN), (dict(codes=at(1) + 8), ALIGN),
+    (dict(scales=at(2) + 2), ALIGN), (dict(num_rows=at(3) + 2), ALIGN)])
+def test_quantize_refusals(lib, change, want):
+    assert quantize(lib, **change) == want
+
+
+def norm(lib, **change):
+    a = dict(X=at(0), residual=at(1), weight=at(2), H=at(3), Y=at(4), codes=at(5), scales=at(6),
+             M=4, K=256, eps=1e-6, dtype=2, weight_dtype=2)
+    a.update(change)
+    return lib.w8a8_rms_norm(*a.values(), None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(M=0), OK), (dict(M=0, X=None), OK), (dict(M=-1), ARG), (dict(K=0), ARG),
+    (dict(eps=0.0), ARG), (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG),
+    (dict(eps=float("inf")), ARG), (dict(M=0, eps=0.0), ARG), (dict(dtype=3), ARG),
+    (dict(weight_dtype=1), ARG), (dict(dtype=0, weight_dtype=2), ARG),
+    (dict(X=None), ARG), (dict(weight=None), ARG), (dict(codes=None), ARG),
+    (dict(scales=None), ARG), (dict(H=None, Y=None, codes=None, scales=None), ARG),
+    (dict(Y=at(0)), ARG), (dict(Y=at(1)), ARG), (dict(Y=at(2)), ARG), (dict(Y=at(3)), ARG),
+    (dict(H=at(0) + 512), ARG), (dict(H=at(1) + 16), ARG), (dict(H=at(2)), ARG),
+    (dict(codes=at(0)), ARG), (dict(scales=at(2) + 256), ARG), (dict(scales=at(5)), ARG),
+    (dict(K=200), SHAPE), (dict(K=(1 << 15) + 16), SHAPE), (dict(M=BIG), SHAPE),
+    # 64, 256, 1024 threads a row
+    (dict(M=(1 << 26) + 8, K=16), SHAPE), (dict(M=(1 << 24), K=4096), SHAPE),
+    (dict(M=(1 << 22), K=16384), SHAPE),
+    (dict(X=at(0) + 2), ALIGN), (dict(residual=at(1) + 8), ALIGN), (dict(weight=at(2) + 8), ALIGN),
+    (dict(H=at(3) + 8), ALIGN), (dict(Y=at(4) + 8), ALIGN), (dict(codes=at(5) + 8), ALIGN),
+    (dict(scales=at(6) + 2), ALIGN)])
+def test_norm_refusals(lib, change, want):
+    # rows past 64 GB apart: addresses of the large cases do not meet
+    if change.get("M", 0) > 1 << 20 and want == SHAPE:
+        change = dict(change, **{k: i << 44 for i, k in enumerate(
+            ("X", "residual", "weight", "H", "Y", "codes", "scales"), 1)})
+    assert norm(lib, **change) == want
+
+
+def gemm(lib, **change):
+    a = dict(X=at(0), xs=at(1), W=at(2), ws=at(3), Y=at(4), M=4, N=300, K=256, block=128, dtype=2)
+    a.update(change)
+    return lib.w8a8_gemm(*a.values(), None)
+
+
+GEMM = [
+    (dict(N=0), OK), (dict(N=0, X=None, Y=None), OK), (dict(N=-1), ARG), (dict(K=0), ARG),
+    (dict(block=64), ARG), (dict(dtype=4), ARG), (dict(X=None), ARG), (dict(xs=None), ARG),
+    (dict(W=None), ARG), (dict(ws=None), ARG), (dict(Y=None), ARG), (dict(Y=at(0)), ARG),
+    (dict(Y=at(1)), ARG), (dict(Y=at(2) + 300 * 256 - 2), ARG), (dict(Y=at(3)), ARG),
+    (dict(K=40), SHAPE), (dict(K=(1 << 17) + 16), SHAPE), (dict(N=BIG), SHAPE),
+    (dict(X=at(0) + 8), ALIGN), (dict(xs=at(1) + 2), ALIGN), (dict(W=at(2) + 8), ALIGN),
+    (dict(ws=at(3) + 2), ALIGN), (dict(Y=at(4) + 1), ALIGN), (dict(Y=at(4) + 2, dtype=0), ALIGN)]
+
+
+@pytest.mark.parametrize("change,want", GEMM + [
+    (dict(M=0), OK), (dict(M=-1), ARG), (dict(M=BIG), SHAPE)])
+def test_gemm_refusals(lib, change, want):
+    assert gemm(lib, **change) == want
+
+
+def grouped(lib, **change):
+    a = dict(X=at(0), xs=at(1), token_index=at(5), expert_offsets=at(6), W=at(2), ws=at(3),
+             Y=at(4), T=4, R=8, E=3, N=300, K=256, block=128, dtype=2)
+    a.update(change)
+    return lib.w8a8_gemm_grouped(*a.values(), None)
+
+
+@pytest.mark.parametrize("change,want", GEMM + [
+    (dict(R=0), OK), (dict(R=0, T=0), OK), (dict(R=-1), ARG), (dict(T=-1), ARG), (dict(T=0), ARG),
+    (dict(E=0), ARG), (dict(token_index=None), ARG), (dict(expert_offsets=None), ARG),
+    (dict(Y=at(5)), ARG), (dict(Y=at(6)), ARG), (dict(R=BIG), SHAPE), (dict(T=BIG), SHAPE),
+    (dict(E=65536), SHAPE), (dict(token_index=at(5) + 2), ALIGN),
+    (dict(expert_offsets=at(6) + 2), ALIGN)])
+def test_grouped_refusals(lib, change, want):
+    assert grouped(lib, **change) == want
+
+
+def test_products_past_the_grid(lib):
+    far = {k: i << 50 for i, k in enumerate(("X", "xs", "W", "ws", "Y"), 1)}
+    assert gemm(lib, M=BIG - 1, N=BIG - 1, K=16, **far) == SHAPE
+
+
+def test_kernel_choice(lib):
+    assert lib.w8a8_kernel(1, 1, 4096, 7168, 2) == pkg.W8A8_KERNEL_SKINNY
+    for bad in ((0, 1, 64, 64, 0), (1, 0, 64, 64, 0), (1, 1, 0, 64, 0), (1, 1, 64, 40, 0),
+                (1, 1, 64, 64, 3), (BIG, 1, 64, 64, 0), (1, 65536, 64, 64, 0)):
+        assert lib.w8a8_kernel(*bad) == 0
+
+
+@pytest.mark.parametrize("N,K,spread", [(1, 16, 0), (128, 128, 0), (129, 144, 10), (300, 400, 40)])
+def test_weights_quantizer_is_the_oracles(N, K, spread):
+    rng = np.random.default_rng(N)
+    W = (rng.standard_normal((N, K)) * np.exp2(rng.uniform(-spread, spread, (N, K)))).astype(np.float32)
+    W[rng.random((N, K)) < 0.1] = 0.0
+    W[0, 0] = -0.0
+    codes, scales = pkg.w8a8_quantize_weights(W)
+    want, want_s = oracle.w8a8.quantize_weights(W)
+    assert np.array_equal(scales, want_s) and np.array_equal(codes, want)
+
+
+def test_weights_quantizer_at_its_ends():
+    # ties, the largest value, nothing but zeros, magnitudes below fp32's normal range
+    q = np.concatenate([oracle.w8a8.E4M3[:127], -oracle.w8a8.E4M3[:127],
+                        (oracle.w8a8.E4M3[:126] + oracle.w8a8.E4M3[1:127]) / 2]).astype(np.float32)
+    W = np.zeros((256, 512), np.float32)
+    W[:128, :128].flat[:q.size] = q
+    W[:128, 128:256] = np.float32(2.0 ** -130)
+    W[128:, 256:384] = np.float32(3e38)
+    W[128:, 384:] = np.float32(2.0 ** -149)
+    codes, scales = pkg.w8a8_quantize_weights(W)
+    want, want_s = oracle.w8a8.quantize_weights(W)
+    assert np.array_equal(scales, want_s) and np.array_equal(codes, want)
+    assert scales[0, 1] == np.float32(2.0 ** -126) and scales[1, 0] == 0
+    for bad in (np.nan, np.inf):
+        W[5, 5] = bad
+        with pytest.raises(pkg.W4A16Error) as refused:
+            pkg.w8a8_quantize_weights(W)
+        assert refused.value.status == NONFINITE
+
+
+def test_weights_quantizer_refusals(lib):
+    W = np.zeros((4, 32), np.float32)
+    c, s = np.full((4, 32), 7, np.uint8), np.full((1, 1), 7, np.float32)
+    p = (W.ctypes.data, c.ctypes.data, s.ctypes.data)
+    assert lib.w8a8_quantize_weights(*p, 4, 32, 64) == ARG
+    assert lib.w8a8_quantize_weights(*p, -1, 32, 128) == ARG
+    assert lib.w8a8_quantize_weights(*p, 4, 0, 128) == ARG
+    assert lib.w8a8_quantize_weights(*p, 4, 24, 128) == SHAPE
+    assert lib.w8a8_quantize_weights(*p, 4, (1 << 17) + 16, 128) == SHAPE
+    assert lib.w8a8_quantize_weights(None, *p[1:], 4, 32, 128) == ARG
+    assert lib.w8a8_quantize_weights(*p, 0, 32, 128) == OK
+    assert np.all(c == 7) and np.all(s == 7)
+    with pytest.raises(TypeError):
+        pkg.w8a8_quantize_weights(W.astype(np.float64))
+
+
+def test_binding_refuses_host_tensors():
+    torch = pytest.importorskip("torch")
+    X, s = torch.zeros(2, 128), torch.zeros(2, 1)
+    c = X.to(torch.float8_e4m3fn)
+    for call in (lambda: pkg.w8a8_quantize(X), lambda: pkg.w8a8_rms_norm(X, X[0]),
+                 lambda: pkg.w8a8_gemm(c, s, c, s[:1]),
+                 lambda: pkg.w8a8_gemm_grouped(c, s, None, None, c[None], s[None, :1])):
+        with pytest.raises(TypeError):
+            call()
