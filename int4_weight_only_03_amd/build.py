@@ -24,14 +24,16 @@ ARCH = "gfx950"
 DEVICE_SOURCES = ["gemv.hip", "gemv_mfma.hip", "tile.hip", "split.hip", "grouped.hip",
                   "small_packed.hip", "read_floor.hip", "skinny.hip", "tile_mx.hip",
                   "moe_route.hip", "moe_limbs.hip", "moe_skinny.hip", "moe_tile.hip",
-                  "moe_combine.hip", "w8a8_rows.hip", "w8a8_norm.hip", "w8a8_skinny.hip"]
+                  "moe_combine.hip", "w8a8_rows.hip", "w8a8_norm.hip", "w8a8_skinny.hip",
+                  "w8a8_tile.hip"]
 HOST_SOURCES = ["w4a16_api.cpp", "w4a16_io.cpp", "moe_api.cpp", "w8a8_api.cpp"]
 # per-source options: the split path's MFMA results stay in VGPRs (the scale
 # FMAs read them directly, no accumulator-register copies); so do the tiled
 # kernel's block sums, which are added to running totals in VGPRs
 EXTRA = {"split.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "w8a8_skinny.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+         "w8a8_skinny.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "w8a8_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def hipcc() -> str:

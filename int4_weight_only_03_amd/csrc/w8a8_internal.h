@@ -53,5 +53,6 @@ struct Gemm8 {
 int gemm8_kernel(long R, long E, long N, long K, int dtype);
 hipError_t launch_gemm8(const Gemm8 &p, hipStream_t stream);
 hipError_t launch_gemm8_skinny(const Gemm8 &p, hipStream_t stream);
+hipError_t launch_gemm8_tile(const Gemm8 &p, hipStream_t stream);
 
 }  // namespace w4a16

@@ -221,21 +221,12 @@ hipError_t run_skinny_type(const Gemm8 &p, hipStream_t stream) {
 
 }  // namespace
 
-int gemm8_kernel(long R, long E, long N, long K, int dtype) {
-  (void)R, (void)E, (void)N, (void)K, (void)dtype;
-  return W8A8_KERNEL_SKINNY;
-}
-
 hipError_t launch_gemm8_skinny(const Gemm8 &p, hipStream_t stream) {
   switch (p.dtype) {
     case W4A16_DTYPE_F32: return run_skinny_type<float>(p, stream);
     case W4A16_DTYPE_F16: return run_skinny_type<_Float16>(p, stream);
     default: return run_skinny_type<Bf16>(p, stream);
   }
-}
-
-hipError_t launch_gemm8(const Gemm8 &p, hipStream_t stream) {
-  return launch_gemm8_skinny(p, stream);
 }
 
 }  // namespace w4a16

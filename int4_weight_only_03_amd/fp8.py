@@ -26,6 +26,7 @@ from .moe import _code, _launch, _pointer, _tensor
 
 BLOCK = 128
 W8A8_KERNEL_SKINNY = 1
+W8A8_KERNEL_TILE = 2
 
 # codes [M][K], scales fp32 [M][ceil(K / 128)]
 W8A8Rows = namedtuple("W8A8Rows", "codes scales")

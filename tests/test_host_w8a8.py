@@ -122,6 +122,7 @@ def test_products_past_the_grid(lib):
 
 def test_kernel_choice(lib):
     assert lib.w8a8_kernel(1, 1, 4096, 7168, 2) == pkg.W8A8_KERNEL_SKINNY
+    assert lib.w8a8_kernel(4096, 1, 4096, 7168, 2) == pkg.W8A8_KERNEL_TILE
     for bad in ((0, 1, 64, 64, 0), (1, 0, 64, 64, 0), (1, 1, 0, 64, 0), (1, 1, 64, 40, 0),
                 (1, 1, 64, 64, 3), (BIG, 1, 64, 64, 0), (1, 65536, 64, 64, 0)):
         assert lib.w8a8_kernel(*bad) == 0
