@@ -10,16 +10,16 @@
 // instructions instead.
 //
 // A workgroup's GU x GT waves take 16 WU slots by 16 WT rows of W each.  Stages of one block
-// of features: rows of 128 bytes come to LDS by direct copies one stage ahead, in two images,
-// with one barrier a stage.  The scales' products, 4 stages of a slot and 128 rows of W at a
-// time, are formed by one thread each and pass through LDS as well, one such run ahead.
+// of features: rows of 128 bytes, and the slots' scales, come to LDS by direct copies one
+// stage ahead, in two images.
 //
 // Tiles are dealt so that each XCD works a contiguous run of them (the hardware deals
-// workgroups round-robin over the 8 XCDs), slots of an expert fastest.
+// workgroups round-robin over the 8 XCDs); see in_band for their order.
 
 #include "w8a8_common.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace w4a16 {
 namespace {
@@ -36,11 +36,13 @@ struct TileArgs {
   const float *ws;
   void *Y;
   int rows_x, R, E, N, K, KB, NB, tiles_n;
-  int vec;  // outputs that rows of Y begin and end at a multiple of: 8, 4 or 1
+  bool vec;  // rows of Y begin and end at 16 bytes
 };
 
-__device__ __forceinline__ void t8_wait_copies() {
-  __builtin_amdgcn_s_waitcnt(0x70 | (15 << 8));  // vmcnt(0)
+template <int VM>
+__device__ __forceinline__ void t8_wait_copies() {  // at most VM still in flight
+  static_assert(VM >= 0 && VM < 64, "wait count");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70 | (15 << 8));
 }
 __device__ __forceinline__ void t8_wait_lds() {
   __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | 0x70);  // lgkmcnt(0)
@@ -59,6 +61,11 @@ __device__ __forceinline__ void t8_copy16(const uint8_t *base, uint32_t offset, 
 }
 __device__ __forceinline__ void t8_copy16(const uint8_t *from, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 1\n\tglobal_load_lds_dwordx4 %0, off"
+               :: "v"(from), "s"(lds) : "memory", "m0");
+}
+
+__device__ __forceinline__ void t8_copy4(const float *from, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 1\n\tglobal_load_lds_dword %0, off"
                :: "v"(from), "s"(lds) : "memory", "m0");
 }
 
@@ -101,21 +108,36 @@ __device__ __forceinline__ f32x4 block_sum(const Operand<true> &w, const Operand
   return d;
 }
 
-template <int WU, int WT, int GU, int GT, typename OT, bool kExact>
-__global__ void __launch_bounds__(64 * GU * GT, 2) gemm8_tile(TileArgs a) {
-  constexpr int kWaves = GU * GT, kThreads = 64 * kWaves;
+// Tile `i` of `tiles_m` x `tiles_n`: bands of kBand blocks of slots, in a band the blocks of
+// slots fastest, so that the 32 tiles that an XCD holds at once are about 4 x 8 and share
+// their operands in its L2.
+constexpr int kBand = 4;
+__device__ __forceinline__ void in_band(long i, int tiles_m, int tiles_n, int &bm, int &bn) {
+  const long band = i / (long(kBand) * tiles_n);
+  const int within = int(i - band * kBand * tiles_n);
+  const int high = std::min(kBand, tiles_m - int(band) * kBand);
+  bm = int(band) * kBand + within % high;
+  bn = within / high;
+}
+
+template <int WU, int WT, int GU, int GT, int G, int S, typename OT, bool kExact>
+__global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * GT / 4 : 2) gemm8_tile(TileArgs a) {
+  constexpr int kWaves = GU * GT;  // of a group
   constexpr int TM = 16 * WU * GU, TN = 16 * WT * GT;  // slots and rows of W of a tile
   constexpr int kX = TM * 128, kImage = kX + TN * 128;
-  constexpr int kSN = (TN + 127) / 128;               // blocks of W rows
-  constexpr int kS = 4 * kSN * TM;                    // scales' products of 4 stages
-  static_assert(kSN * TM <= kThreads, "a thread forms 4 products");
-  static_assert(128 % (16 * WT) == 0 && (TN % 128 == 0 || 128 % TN == 0), "blocks of W rows");
+  static_assert(128 % (16 * WT) == 0, "a wave's rows of W share their scales");
+  constexpr int kS = TM;  // slots' scales in LDS
+  static_assert(TM % kWaves == 0 && TM / kWaves <= 64, "a wave copies its share of the scales");
   // Row r at 128 r, logical chunk x (16 bytes) at chunk x ^ ((r / 2) % 8), so that the 16
   // rows an operand read touches fall in distinct banks.
-  __shared__ __align__(16) unsigned char mem[2 * kImage];
-  __shared__ __align__(16) float scale[2 * kS];
+  __shared__ __align__(16) unsigned char mem[S * G * kImage];
+  constexpr int kWB = (TN + 127) / 128;  // blocks of W rows
+  static_assert((TN % 128 == 0 || 128 % TN == 0) && kWB <= kWaves, "blocks of W rows");
+  __shared__ __align__(16) float scale[S * G * kS];  // of the slots, by blocks
+  __shared__ __align__(16) float wscale[2 * kWB * 64];  // of W's blocks, by runs of 64
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kg = G == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 6) / kWaves;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) - kg * kWaves;
   const int c = lane & 15, R = lane >> 4;
   const int wu = wave % GU, wt = wave / GU;
 
@@ -130,9 +152,7 @@ __global__ void __launch_bounds__(64 * GU * GT, 2) gemm8_tile(TileArgs a) {
       const long tile = long(blockIdx.x & 7) * run + index;
       if (index >= run || tile >= tiles) return;  // uniform over the workgroup
       it = find_item(a.offsets, a.E, a.R, TM, int(tile / a.tiles_n));
-      const int within = int(tile - (tile / a.tiles_n - it.block) * a.tiles_n);
-      bm = within % it.blocks;
-      bn = within / it.blocks;
+      in_band(tile - (tile / a.tiles_n - it.block) * a.tiles_n, it.blocks, a.tiles_n, bm, bn);
       e = it.e;
       expert_slots(a.offsets, e, a.R, e0, e1);
     } else {
@@ -140,8 +160,7 @@ __global__ void __launch_bounds__(64 * GU * GT, 2) gemm8_tile(TileArgs a) {
       const long tiles = long(tiles_m) * a.tiles_n, run = (tiles + 7) / 8;
       const long tile = long(blockIdx.x & 7) * run + index;
       if (index >= run || tile >= tiles) return;
-      bm = int(tile % tiles_m);
-      bn = int(tile / tiles_m);
+      in_band(tile, tiles_m, a.tiles_n, bm, bn);
     }
   }
   const int row0 = e0 + bm * TM, rows = std::min(TM, e1 - row0);
@@ -151,84 +170,72 @@ __global__ void __launch_bounds__(64 * GU * GT, 2) gemm8_tile(TileArgs a) {
   // Copies: wave w issues those of 8 rows each from w on, kWaves apart, of both operands.
   // Lane i copies 16 bytes of row 8 j + i / 8.  Slots past the item repeat its last, rows of W
   // past N repeat row N - 1.  LDS row 16 t + i of a wave's strip of W holds its row
-  // 16 (i / 4) + 4 t + i % 4 (of 64; 8 (i / 4) ... of 32), so that a lane's sums are
-  // neighbouring outputs.
-  constexpr int kXC = TM / 8 / kWaves, kWC = TN / 8 / kWaves;
-  static_assert(TM % (8 * kWaves) == 0 && TN % (8 * kWaves) == 0, "copies deal out evenly");
+  // 4 WT (i / 4) + 4 t + i % 4, so that a lane's sums are neighbouring outputs.
+  constexpr int kXC = TM / 8 / kWaves, kWC = TN / 8 / kWaves, kAll = kXC + kWC + 1;  // 1: scales
+  static_assert(TM % (8 * kWaves) == 0 && TN % (8 * kWaves) == 0 && kWaves % 2 == 0,
+                "copies deal out evenly");
   const uint8_t *wbase = a.W + (long(e) * a.N + n0) * K;
   const uint8_t *xat[kXC];
   uint32_t wat[kWC];
 #pragma unroll
   for (int j = 0; j < kXC; ++j) {
-    const int r = 8 * (wave + j * kWaves) + lane / 8;
-    long row = row0 + std::min(r, rows - 1);
+    long row = row0 + std::min(8 * (wave + j * kWaves) + lane / 8, rows - 1);
     if (a.token_index) row = std::min(std::max(a.token_index[row], 0), a.rows_x - 1);
-    xat[j] = a.X + row * K + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+    xat[j] = a.X + row * K;
   }
 #pragma unroll
   for (int j = 0; j < kWC; ++j) {
     const int r = 8 * (wave + j * kWaves) + lane / 8;
     const int strip = r / (16 * WT), t = r % (16 * WT) / 16, i = r % 16;
     const int n = std::min(16 * WT * strip + 4 * WT * (i / 4) + 4 * t + i % 4, a.N - 1 - n0);
-    wat[j] = uint32_t(n) * uint32_t(a.K) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+    wat[j] = uint32_t(n) * uint32_t(a.K);
   }
+  // the chunk that a lane copies, the same in all of a wave's copies: their blocks of 8 rows
+  // are all even or all odd
+  const uint32_t chunk = 16 * ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));
   const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>((const t8_lds_void *)mem));
-  auto copy = [&](int p) {
-    const uint32_t at = uint32_t(p & 1) * kImage;
-    const long k0 = long(p) * kBlock8;
-    const uint8_t *w = wbase + k0;
-    if (kBlock8 * (p + 1) <= a.K) {
+  // the ring of S stages of G blocks
+  auto image_of = [&](int p) { return uint32_t(p & (S * G - 1)); };
+  // where a lane reads in its rows for block p; behind their end (the last block of K may be
+  // shorter than 128) their last 16 bytes once more
+  auto offset_of = [&](int p) { return std::min(uint32_t(p) * kBlock8 + chunk, uint32_t(a.K) - 16); };
+  // copy j of block p's slots and of its rows of W
+  auto copy_x = [&](int j, int p, uint32_t at) {
+    t8_copy16(xat[j] + at, lds0 + image_of(p) * kImage + 1024 * (wave + j * kWaves));
+  };
+  auto copy_w = [&](int j, int p, uint32_t at) {
+    t8_copy16(wbase, wat[j] + at, lds0 + image_of(p) * kImage + kX + 1024 * (wave + j * kWaves));
+  };
+  // zeros in place of W's codes that were copied from behind the rows' end, and of X's
+  auto clear_behind = [&](int p, uint32_t to, int copies) {
+    if (uint32_t(p) * kBlock8 + chunk < uint32_t(a.K)) return;
 #pragma unroll
-      for (int j = 0; j < kXC; ++j) t8_copy16(xat[j] + k0, lds0 + at + 1024 * (wave + j * kWaves));
-#pragma unroll
-      for (int j = 0; j < kWC; ++j) t8_copy16(w, wat[j], lds0 + at + kX + 1024 * (wave + j * kWaves));
-    } else {
-      // the last block of K, shorter: zeros behind the row's end
-      const u32x4m none = {0, 0, 0, 0};
-      auto part = [&](const uint8_t *from, uint32_t to, int r) {
-        const long k = k0 + 16 * ((lane & 7) ^ ((r >> 1) & 7));
-        if (k < K)
-          t8_copy16(from, lds0 + to);
-        else
-          *reinterpret_cast<u32x4m *>(mem + to + 16 * lane) = none;
-      };
-#pragma unroll
-      for (int j = 0; j < kXC; ++j)
-        part(xat[j] + k0, at + 1024 * (wave + j * kWaves), 8 * (wave + j * kWaves) + lane / 8);
-#pragma unroll
-      for (int j = 0; j < kWC; ++j)
-        part(w + wat[j], at + kX + 1024 * (wave + j * kWaves), 8 * (wave + j * kWaves) + lane / 8);
-    }
+    for (int j = 0; j < copies; ++j)
+      *reinterpret_cast<u32x4m *>(mem + image_of(p) * kImage + to + 1024 * (wave + j * kWaves) +
+                                  16 * lane) = u32x4m{0, 0, 0, 0};
   };
 
-  // scales' products: thread i those of slot i % TM and block i / TM of the tile's W rows
-  const bool forms = tid < kSN * TM;
-  const float *sx = a.xs, *sw = a.ws;
-  if (forms) {
-    const int i = row0 + std::min(tid % TM, rows - 1);
-    const long row = a.token_index ? std::min(std::max(a.token_index[i], 0), a.rows_x - 1) : i;
+  // scales: every wave copies those of as many slots (each lane's lies in a cache line of its
+  // own, which costs as much as 16 bytes)
+  constexpr int kSC = kS / kWaves;
+  const uint32_t scale0 = uint32_t(reinterpret_cast<uintptr_t>((const t8_lds_void *)scale));
+  const float *sx = a.xs;
+  {
+    long row = row0 + std::min(kSC * wave + lane, rows - 1);
+    if (a.token_index) row = std::min(std::max(a.token_index[row], 0), a.rows_x - 1);
     sx += row * a.KB;
-    sw += (long(e) * a.NB + std::min(n0 / kBlock8 + tid / TM, a.NB - 1)) * a.KB;
   }
-  f32x4 fx, fw;
-  auto load_scales = [&](int p) {  // of stages p .. p + 3; those past the last repeat it
-    if (!forms) return;
-    if (p + 4 <= a.KB) {
-      fx = *reinterpret_cast<const f32x4a4 *>(sx + p);
-      fw = *reinterpret_cast<const f32x4a4 *>(sw + p);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        fx[i] = sx[std::min(p + i, a.KB - 1)];
-        fw[i] = sw[std::min(p + i, a.KB - 1)];
-      }
-    }
+  auto copy_scales = [&](int p) {
+    if (lane < kSC)
+      t8_copy4(sx + std::min(p, a.KB - 1), scale0 + (image_of(p) * kS + kSC * wave) * 4);
   };
-  auto store_scales = [&](int p) {
-    if (!forms) return;
-    float *to = scale + (p >> 2 & 1) * kS + tid;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) to[i * kSN * TM] = fx[i] * fw[i];
+  // scales of W: wave i copies those of block i of the tile's rows, of 64 blocks of K at once
+  const uint32_t wscale0 = uint32_t(reinterpret_cast<uintptr_t>((const t8_lds_void *)wscale));
+  auto copy_wscales = [&](int p) {
+    if (kg > 0 || wave >= kWB) return;
+    const long block = long(e) * a.NB + std::min(n0 / kBlock8 + wave, a.NB - 1);
+    t8_copy4(a.ws + block * a.KB + std::min(p + lane, a.KB - 1),
+             wscale0 + ((p >> 6 & 1) * kWB + wave) * 256);
   };
 
   // operand reads: row 16 u + c of the wave's slots, chunks R and 4 + R
@@ -236,60 +243,151 @@ __global__ void __launch_bounds__(64 * GU * GT, 2) gemm8_tile(TileArgs a) {
 #pragma unroll
   for (int q = 0; q < 2; ++q) read[q] = uint32_t(c * 128 + 16 * ((4 * q + R) ^ ((c >> 1) & 7)));
   const uint32_t xread = uint32_t(16 * WU * wu) * 128, wread = kX + uint32_t(16 * WT * wt) * 128;
-  const int sread = (16 * WT * wt / kBlock8) * TM + 16 * WU * wu + c;
+  const int sread = 16 * WU * wu + c;
 
+  constexpr int kDelay = 2;
   f32x4 acc[WU][WT];
 #pragma unroll
   for (int u = 0; u < WU; ++u)
 #pragma unroll
     for (int t = 0; t < WT; ++t) acc[u][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  // The products of stage p, and, between them, the copies of stage p + 1 (all at once they
+  // would hold up the wave for as long as the memory pipeline takes them).  The FMAs of a sum
+  // stand kDelay products behind it; slots are fetched kAhead steps of WT products ahead.
+  constexpr int kAhead = WU > 1 ? 2 : 1, kN = WU * WT, kIssue = kN / 2;
+  u32x4m wraw[WT][2];
+  auto fetch_w = [&](int t, int p) {
+    const unsigned char *img = mem + image_of(p) * kImage + wread + 2048 * t;
+    wraw[t][0] = *reinterpret_cast<const u32x4m *>(img + read[0]);
+    wraw[t][1] = *reinterpret_cast<const u32x4m *>(img + read[1]);
+  };
   auto multiply = [&](int p) {
-    const unsigned char *img = mem + (p & 1) * kImage;
-    const float *s = scale + (p >> 2 & 1) * kS + (p & 3) * kSN * TM + sread;
-    Operand<kExact> w[WT];
+    const unsigned char *img = mem + image_of(p) * kImage;
+    // behind the last stage it is copied once more, into images that nobody reads again
+    const uint32_t xoff = offset_of(p + (S - 1) * G), woff = offset_of(p + S * G);
+    const float *s = scale + int(image_of(p)) * kS + sread;
+    const float fw = wscale[((p >> 6 & 1) * kWB + 16 * WT * wt / kBlock8) * 64 + (p & 63)];
+    Operand<kExact> w[WT], x[kAhead + 1];
 #pragma unroll
-    for (int t = 0; t < WT; ++t)
-      w[t].set(*reinterpret_cast<const u32x4m *>(img + wread + 2048 * t + read[0]),
-               *reinterpret_cast<const u32x4m *>(img + wread + 2048 * t + read[1]));
+    for (int t = 0; t < WT; ++t) w[t].set(wraw[t][0], wraw[t][1]);
+    f32x4 d[kDelay];
+    float f[kAhead + 1], g = 0.0f;
+    auto fetch = [&](int u) {
+      x[u % (kAhead + 1)].set(*reinterpret_cast<const u32x4m *>(img + xread + 2048 * u + read[0]),
+                              *reinterpret_cast<const u32x4m *>(img + xread + 2048 * u + read[1]));
+      f[u % (kAhead + 1)] = s[16 * u];
+    };
 #pragma unroll
-    for (int u = 0; u < WU; ++u) {
-      Operand<kExact> x;
-      x.set(*reinterpret_cast<const u32x4m *>(img + xread + 2048 * u + read[0]),
-            *reinterpret_cast<const u32x4m *>(img + xread + 2048 * u + read[1]));
-      const float f = s[16 * u];
+    for (int u = 0; u < kAhead; ++u) fetch(u);
+    __builtin_amdgcn_sched_barrier(0);
+    copy_scales(p + (S - 1) * G);
 #pragma unroll
-      for (int t = 0; t < WT; ++t) {
-        const f32x4 d = block_sum(w[t], x);
+    for (int i = 0; i < kN + kDelay; ++i) {
+      const int u = i / WT, t = i % WT;
+      f32x4 now;
+      if (i < kN) now = block_sum(w[t], x[u % (kAhead + 1)]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i >= kDelay) {
+        const int v = (i - kDelay) / WT, o = (i - kDelay) % WT;
+        if (o == 0) g = f[v % (kAhead + 1)] * fw;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[u][t][i] = fmaf(f, d[i], acc[u][t][i]);
+        for (int r = 0; r < 4; ++r)
+          acc[v][o][r] = fmaf(g, d[i % kDelay][r], acc[v][o][r]);
+        // here, not sunk to where the sums are used next: their products would stay in
+        // registers till then
+        asm volatile("" : "+v"(acc[v][o]));
       }
+      if (i < kN) d[i % kDelay] = now;
+      if (i < kN && t == kDelay - 1 && u + kAhead < WU) fetch(u + kAhead);
+#pragma unroll
+      for (int j = 0; j < kXC + kWC; ++j) {
+        if (j * kIssue / (kXC + kWC) != i) continue;
+        if (j < kXC)
+          copy_x(j, p + (S - 1) * G, xoff);
+        else
+          copy_w(j - kXC, p + S * G, woff);
+      }
+      if (i >= kN - WT && i < kN) fetch_w(t, p + G);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
   // At a stage's start its copies have landed in this wave; past the barrier they have in
   // every wave, and every wave is past the stage before, whose image is then filled again.
-  load_scales(0);
-  store_scales(0);
-  copy(0);
-  for (int p = 0; p < a.KB; ++p) {
-    t8_wait_copies();
+  copy_wscales(0);
+#pragma unroll
+  for (int j = 0; j < kWC; ++j) copy_w(j, kg, offset_of(kg));
+  for (int q = 0; q < S - 1; ++q) {
+    const int p = q * G + kg;
+    copy_scales(p);
+#pragma unroll
+    for (int j = 0; j < kXC; ++j) copy_x(j, p, offset_of(p));
+#pragma unroll
+    for (int j = 0; j < kWC; ++j) copy_w(j, p + G, offset_of(p + G));
+  }
+  // waits until the copies of all but the last n stages are here
+  auto landed = [&](auto n) {
+    constexpr int kStages = decltype(n)::value;
+    t8_wait_copies<kStages * kAll>();
+  };
+  landed(std::integral_constant<int, S - 1>());
+  if (kBlock8 * (kg + 1) > a.K) clear_behind(kg, kX, kWC);
+  t8_wait_lds();
+  t8_barrier();
+#pragma unroll
+  for (int t = 0; t < WT; ++t) fetch_w(t, kg);
+  // the first stage in which a block may be short
+  const int last = a.K % kBlock8 ? a.KB - 2 * G : a.KB;
+  for (int q = 0; q < a.KB; q += G) {
+    const int p = q + kg;  // the group's block
+    landed(std::integral_constant<int, S - 2>());
+    if (q >= last) {
+      clear_behind(p, 0, kXC);
+      clear_behind(p + G, kX, kWC);
+    }
     t8_wait_lds();
     t8_barrier();
-    if ((p & 3) == 3 && p + 1 < a.KB) store_scales(p + 1);
-    if (p + 1 < a.KB) copy(p + 1);
-    if ((p & 3) == 0 && p + 4 < a.KB) load_scales(p + 4);
-    multiply(p);
+    if ((q & 63) == 0 && q + 64 < a.KB) copy_wscales(q + 64);
+    if (p < a.KB) multiply(p);
+  }
+  t8_wait_copies<0>();  // the LDS is the next workgroup's, or the sums'
+
+  if constexpr (G > 1) {
+    // the groups' sums, added in their order; group i takes the slots u = i, i + G, ...
+    static_assert(sizeof(mem) >= G * kWaves * WU * WT * 1024, "room for all sums");
+    static_assert(WU % G == 0 || G % WU == 0, "slots deal out evenly");
+    t8_barrier();
+    f32x4 *const sums = reinterpret_cast<f32x4 *>(mem);
+#pragma unroll
+    for (int u = 0; u < WU; ++u)
+#pragma unroll
+      for (int t = 0; t < WT; ++t)
+        sums[((kg * kWaves + wave) * WU * WT + u * WT + t) * 64 + lane] = acc[u][t];
+    t8_wait_lds();
+    t8_barrier();
+#pragma unroll
+    for (int u = 0; u < WU; ++u) {
+      if (u % G != kg) continue;
+#pragma unroll
+      for (int t = 0; t < WT; ++t) {
+        f32x4 v = sums[(wave * WU * WT + u * WT + t) * 64 + lane];
+#pragma unroll
+        for (int i = 1; i < G; ++i)
+          v += sums[((i * kWaves + wave) * WU * WT + u * WT + t) * 64 + lane];
+        acc[u][t] = v;
+      }
+    }
   }
 
   OT *y = static_cast<OT *>(a.Y);
 #pragma unroll
   for (int u = 0; u < WU; ++u) {
     const int m = 16 * WU * wu + 16 * u + c;
-    if (m >= rows) continue;
+    if (m >= rows || u % G != kg) continue;
     const int n = n0 + 16 * WT * wt + 4 * WT * R;
     OT *to = y + long(row0 + m) * a.N + n;
-    if (a.vec == 8) {
+    if (a.vec) {
       constexpr int kV = 16 / sizeof(OT);
       struct alignas(16) Some {
         OT v[kV];
@@ -310,7 +408,7 @@ __global__ void __launch_bounds__(64 * GU * GT, 2) gemm8_tile(TileArgs a) {
   }
 }
 
-template <int WU, int WT, int GU, int GT, typename OT, bool kExact>
+template <int WU, int WT, int GU, int GT, int G, int S, typename OT, bool kExact>
 hipError_t run_tile8(const Gemm8 &p, hipStream_t stream) {
   constexpr int TM = 16 * WU * GU, TN = 16 * WT * GT;
   TileArgs a;
@@ -330,13 +428,13 @@ hipError_t run_tile8(const Gemm8 &p, hipStream_t stream) {
   a.NB = blocks8(p.N);
   a.tiles_n = int((long(p.N) + TN - 1) / TN);
   constexpr int kV = 16 / sizeof(OT);
-  a.vec = p.N % kV == 0 && reinterpret_cast<uintptr_t>(p.Y) % 16 == 0 ? 8 : 1;
+  a.vec = p.N % kV == 0 && reinterpret_cast<uintptr_t>(p.Y) % 16 == 0;
   const long items =
       p.expert_offsets ? max_items(p.R, p.E, TM) : (long(p.R) + TM - 1) / TM;
   const long tiles = items * a.tiles_n;
-  if (tiles > kMaxBlocks * 4 / (GU * GT)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((gemm8_tile<WU, WT, GU, GT, OT, kExact>), dim3(unsigned((tiles + 7) / 8 * 8)),
-                     dim3(64 * GU * GT), 0, stream, a);
+  if (tiles > kMaxBlocks * 4 / (GU * GT * G)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((gemm8_tile<WU, WT, GU, GT, G, S, OT, kExact>), dim3(unsigned((tiles + 7) / 8 * 8)),
+                     dim3(64 * GU * GT * G), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -355,9 +453,9 @@ hipError_t launch_gemm8(const Gemm8 &p, hipStream_t stream) {
 
 hipError_t launch_gemm8_tile(const Gemm8 &p, hipStream_t stream) {
   switch (p.dtype) {
-    case W4A16_DTYPE_F32: return run_tile8<4, 4, 2, 2, float, true>(p, stream);
-    case W4A16_DTYPE_F16: return run_tile8<8, 4, 2, 4, _Float16, false>(p, stream);
-    default: return run_tile8<8, 4, 2, 4, Bf16, false>(p, stream);
+    case W4A16_DTYPE_F32: return run_tile8<4, 4, 2, 2, 1, 2, float, true>(p, stream);
+    case W4A16_DTYPE_F16: return run_tile8<8, 4, 2, 4, 1, 2, _Float16, false>(p, stream);
+    default: return run_tile8<8, 4, 2, 4, 1, 2, Bf16, false>(p, stream);
   }
 }
 
