@@ -148,10 +148,11 @@ int w8a8_gemm_grouped(const uint8_t *X, const float *xs, const int32_t *token_in
 #define W8A8_KERNEL_TILE 2   /* many: tiles through LDS; 16-bit outputs on the fp8 matrix
                                 instructions, fp32 outputs on fp16 ones */
 
-/* The kernel for R rows or slots over E experts (1: w8a8_gemm) of N rows (one of
- * W8A8_KERNEL_*); 0 for extents that are refused or a no-op and for an unknown dtype.
- * Host only. */
-int w8a8_kernel(int64_t R, int64_t E, int64_t N, int64_t K, int32_t dtype);
+/* The kernel (one of W8A8_KERNEL_*) of w8a8_gemm for R rows (E = 0), or of
+ * w8a8_gemm_grouped for R slots over E experts: the skinny one for up to 4 rows, or 10 slots
+ * per expert (of the fewer of R and E).  0 for extents that are refused or a no-op.  Host
+ * only. */
+int w8a8_kernel(int64_t R, int64_t E);
 
 #ifdef __cplusplus
 }

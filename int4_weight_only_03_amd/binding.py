@@ -124,7 +124,7 @@ _SIGS_W8A8 = {
                   [ctypes.c_void_p], ctypes.c_int),
     "w8a8_gemm_grouped": ([ctypes.c_void_p] * 7 + [ctypes.c_int64] * 5 + [ctypes.c_int32] * 2 +
                           [ctypes.c_void_p], ctypes.c_int),
-    "w8a8_kernel": ([ctypes.c_int64] * 4 + [ctypes.c_int32], ctypes.c_int),
+    "w8a8_kernel": ([ctypes.c_int64] * 2, ctypes.c_int),
 }
 
 

@@ -217,9 +217,9 @@ int w8a8_gemm_grouped(const uint8_t *X, const float *xs, const int32_t *token_in
   return gemm(X, xs, token_index, expert_offsets, W, ws, Y, T, R, E, N, K, dtype, stream);
 }
 
-int w8a8_kernel(int64_t R, int64_t E, int64_t N, int64_t K, int32_t dtype) {
-  if (gemm_extents(R, R, E, N, K, W8A8_BLOCK, dtype) != W4A16_OK || R == 0 || N == 0) return 0;
-  return w4a16::gemm8_kernel(long(R), long(E), long(N), long(K), dtype);
+int w8a8_kernel(int64_t R, int64_t E) {
+  if (R <= 0 || E < 0 || R > W8A8_MAX_M || E > 65535) return 0;
+  return w4a16::gemm8_kernel(long(R), long(E), E > 0);
 }
 
 }  // extern "C"

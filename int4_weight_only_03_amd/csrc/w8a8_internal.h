@@ -50,7 +50,8 @@ struct Gemm8 {
   void *Y;
   int rows_x, R, E, N, K, dtype;
 };
-int gemm8_kernel(long R, long E, long N, long K, int dtype);
+// W8A8_KERNEL_*: the kernel for R rows of one expert, or R slots over E of them
+int gemm8_kernel(long R, long E, bool grouped);
 hipError_t launch_gemm8(const Gemm8 &p, hipStream_t stream);
 hipError_t launch_gemm8_skinny(const Gemm8 &p, hipStream_t stream);
 hipError_t launch_gemm8_tile(const Gemm8 &p, hipStream_t stream);

@@ -216,7 +216,11 @@ hipError_t run_skinny(const Gemm8 &p, hipStream_t stream) {
 
 template <typename OT>
 hipError_t run_skinny_type(const Gemm8 &p, hipStream_t stream) {
-  return run_skinny<1, 1, 8, 2, OT>(p, stream);
+  // Waves of a tile and rows of W by whether the workgroups are many (us with 8 waves and 16
+  // rows, 4 and 32: 1 row of 4096 x 7168 7.1, 10.8; 244 slots of 60 experts of 2080 x 1408
+  // 56.8, 36.0; 64 of 32 experts of 4096 x 7168 159, 156).
+  return p.expert_offsets ? run_skinny<1, 2, 4, 2, OT>(p, stream)
+                          : run_skinny<1, 1, 8, 2, OT>(p, stream);
 }
 
 }  // namespace

@@ -19,6 +19,7 @@
 #include "w8a8_common.h"
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 namespace w4a16 {
@@ -388,8 +389,8 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
     const int n = n0 + 16 * WT * wt + 4 * WT * R;
     OT *to = y + long(row0 + m) * a.N + n;
     if (a.vec) {
-      constexpr int kV = 16 / sizeof(OT);
-      struct alignas(16) Some {
+      constexpr int kV = std::min(int(16 / sizeof(OT)), 4 * WT);
+      struct alignas(kV * sizeof(OT)) Some {
         OT v[kV];
       };
 #pragma unroll
@@ -438,24 +439,99 @@ hipError_t run_tile8(const Gemm8 &p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Tiles of `slots` x `rows`, and the time of a launch in which every compute unit has one
+// (us, 56 blocks of K) or `per_cu` of them, by measurement.
+struct Choice {
+  int slots, rows, per_cu;
+  double one, all;
+};
+constexpr Choice kChoices[] = {
+    {16, 32, 1, 7.7, 7.7},      // 4 groups of waves over K, 4 images
+    {32, 32, 1, 9.2, 9.2},      // the same
+    {32, 64, 1, 12.3, 12.3},    // 2 groups, 4 images
+    {64, 64, 1, 16.8, 16.8},    // the same
+    {64, 64, 2, 19.6, 30.0},    // 4 images
+    {64, 128, 1, 25.0, 25.0},   // 4 images
+    {128, 128, 1, 39.2, 39.2},  // 4 images
+    {128, 128, 2, 49.0, 66.0},  // 2 images
+    {256, 256, 1, 100.0, 100.0},
+};
+constexpr Choice kExactChoices[] = {  // fp32 outputs: no more registers for larger tiles
+    {16, 32, 1, 9.5, 9.5},    {32, 32, 1, 12.0, 12.0},  {32, 64, 1, 18.0, 18.0},
+    {64, 64, 1, 23.5, 23.5},  {64, 64, 2, 31.3, 40.0},  {128, 128, 2, 66.0, 110.0},
+};
+
+// The choice of least time: rounds of tiles over 256 compute units.  An expert's last tile
+// is on the average half empty.
+template <int kCount>
+int least(const Choice (&list)[kCount], const Gemm8 &p) {
+  const double experts = p.expert_offsets ? std::min(p.R, p.E) : 1;
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < kCount; ++i) {
+    const Choice &c = list[i];
+    const double items = p.expert_offsets
+                             ? experts * std::max(1.0, p.R / experts / c.slots + 0.5)
+                             : double((long(p.R) + c.slots - 1) / c.slots);
+    const double tiles = items * double((long(p.N) + c.rows - 1) / c.rows);
+    const double rounds = std::floor(tiles / (256 * c.per_cu));
+    const double rest = tiles - rounds * 256 * c.per_cu;
+    const double t = rounds * c.all + (rest <= 0.0 ? 0.0 : rest <= 256.0 ? c.one : c.all);
+    if (i == 0 || t < least) {
+      least = t;
+      best = i;
+    }
+  }
+  return best;
+}
+
+template <typename OT>
+hipError_t run_type8(const Gemm8 &p, hipStream_t stream) {
+  switch (least(kChoices, p)) {
+    case 0: return run_tile8<1, 1, 1, 2, 4, 4, OT, false>(p, stream);
+    case 1: return run_tile8<1, 1, 2, 2, 4, 4, OT, false>(p, stream);
+    case 2: return run_tile8<1, 2, 2, 2, 2, 4, OT, false>(p, stream);
+    case 3: return run_tile8<2, 2, 2, 2, 2, 4, OT, false>(p, stream);
+    case 4: return run_tile8<2, 2, 2, 2, 1, 4, OT, false>(p, stream);
+    case 5: return run_tile8<2, 4, 2, 2, 1, 4, OT, false>(p, stream);
+    case 6: return run_tile8<4, 4, 2, 2, 1, 4, OT, false>(p, stream);
+    case 7: return run_tile8<4, 4, 2, 2, 1, 2, OT, false>(p, stream);
+    default: return run_tile8<8, 4, 2, 4, 1, 2, OT, false>(p, stream);
+  }
+}
+
+hipError_t run_exact8(const Gemm8 &p, hipStream_t stream) {
+  switch (least(kExactChoices, p)) {
+    case 0: return run_tile8<1, 1, 1, 2, 4, 4, float, true>(p, stream);
+    case 1: return run_tile8<1, 1, 2, 2, 4, 4, float, true>(p, stream);
+    case 2: return run_tile8<1, 2, 2, 2, 2, 4, float, true>(p, stream);
+    case 3: return run_tile8<2, 2, 2, 2, 2, 4, float, true>(p, stream);
+    case 4: return run_tile8<2, 2, 2, 2, 1, 4, float, true>(p, stream);
+    default: return run_tile8<4, 4, 2, 2, 1, 2, float, true>(p, stream);
+  }
+}
+
 }  // namespace
 
-int gemm8_kernel(long R, long E, long N, long K, int dtype) {
-  (void)N, (void)K, (void)dtype;
-  return R > 64 * std::max(1L, std::min(R, E)) ? W8A8_KERNEL_TILE : W8A8_KERNEL_SKINNY;
+// Few rows: the skinny kernel.  Of one expert (4096 rows of W x 7168, us skinny against the
+// tiles): 1 row 7.1, 7.4 (fp32 outputs 9.3), 16 rows 10.5, 7.6; of many by their mean (32 of
+// the same): 2 156, 168; 8 167, 182; 16 240, 176.
+int gemm8_kernel(long R, long E, bool grouped) {
+  if (!grouped) return R <= 4 ? W8A8_KERNEL_SKINNY : W8A8_KERNEL_TILE;
+  return R <= 10 * std::max(1L, std::min(R, E)) ? W8A8_KERNEL_SKINNY : W8A8_KERNEL_TILE;
 }
 
 hipError_t launch_gemm8(const Gemm8 &p, hipStream_t stream) {
-  return gemm8_kernel(p.R, p.E, p.N, p.K, p.dtype) == W8A8_KERNEL_TILE
+  return gemm8_kernel(p.R, p.E, p.expert_offsets != nullptr) == W8A8_KERNEL_TILE
              ? launch_gemm8_tile(p, stream)
              : launch_gemm8_skinny(p, stream);
 }
 
 hipError_t launch_gemm8_tile(const Gemm8 &p, hipStream_t stream) {
   switch (p.dtype) {
-    case W4A16_DTYPE_F32: return run_tile8<4, 4, 2, 2, 1, 2, float, true>(p, stream);
-    case W4A16_DTYPE_F16: return run_tile8<8, 4, 2, 4, 1, 2, _Float16, false>(p, stream);
-    default: return run_tile8<8, 4, 2, 4, 1, 2, Bf16, false>(p, stream);
+    case W4A16_DTYPE_F32: return run_exact8(p, stream);
+    case W4A16_DTYPE_F16: return run_type8<_Float16>(p, stream);
+    default: return run_type8<Bf16>(p, stream);
   }
 }
 

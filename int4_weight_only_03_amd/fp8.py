@@ -156,10 +156,10 @@ def w8a8_rms_norm(X, weight, residual=None, eps: float = 1e-6, normed: bool = Fa
     return out
 
 
-def w8a8_kernel(R: int, E: int, N: int, K: int, dtype) -> int:
-    """Kernel of the products below for R rows or slots over E experts of N rows
-    (W8A8_KERNEL_*), 0 for a shape they refuse."""
-    return load().w8a8_kernel(R, E, N, K, _code(dtype))
+def w8a8_kernel(R: int, E: int = 0) -> int:
+    """Kernel of w8a8_gemm for R rows, or of w8a8_gemm_grouped for R slots over E experts
+    (W8A8_KERNEL_*), 0 for extents they refuse."""
+    return load().w8a8_kernel(R, E)
 
 
 def _rows_in(X, scales):

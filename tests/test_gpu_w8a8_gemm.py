@@ -15,9 +15,9 @@ def dev():
     return device()
 
 
-def window(R, E, N, K, dtype):
+def window(R, E, dtype):
     """whether the call's kernel adds up in the fp8 instructions' window"""
-    return pkg.w8a8_kernel(R, E, N, K, TYPES[dtype]) != pkg.W8A8_KERNEL_SKINNY and dtype != "fp32"
+    return pkg.w8a8_kernel(R, E) != pkg.W8A8_KERNEL_SKINNY and dtype != "fp32"
 
 
 def operands(rng, M, N, K, E=None):
@@ -30,7 +30,11 @@ def operands(rng, M, N, K, E=None):
 SHAPES = [(1, 1, 16), (1, 130, 272), (2, 4096, 128), (3, 7, 2064), (16, 300, 384), (17, 129, 144),
           (33, 257, 1040), (61, 512, 896), (64, 64, 4112), (65, 200, 256), (100, 1000, 640),
           (128, 128, 128), (129, 385, 400), (200, 640, 1168), (256, 256, 512), (300, 515, 2080),
-          (513, 777, 272), (1000, 300, 1024)]
+          (513, 777, 272), (1000, 300, 1024),
+          # every tile that the library chooses from, more than 64 blocks of features among them
+          (16, 300, 8464), (200, 640, 8336), (40, 7168, 400), (250, 4096, 1296), (256, 700, 16400),
+          (500, 2100, 400), (500, 4100, 272), (1030, 4100, 656), (2050, 4100, 272),
+          (600, 1500, 8336)]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
@@ -43,7 +47,7 @@ def test_gemm(dev, M, N, K, dtype):
         k = np.float32(2.0 ** -np.ceil(np.log2(np.abs(want).max() / 2 ** 14)))
         xs, want, mag = xs * k, want * k, mag * k
     got = pkg.w8a8_gemm(*on(dev, x, xs, w, ws), dtype=TYPES[dtype])
-    close(got, want, ref.bound(mag, want, K, dtype, window(M, 1, N, K, dtype)), f"{M} {N} {K}")
+    close(got, want, ref.bound(mag, want, K, dtype, window(M, 0, dtype)), f"{M} {N} {K}")
 
 
 def routed(rng, T, E, R, empty=()):
@@ -59,7 +63,9 @@ def routed(rng, T, E, R, empty=()):
 @pytest.mark.parametrize("T,E,R,N,K", [
     (1, 1, 1, 16, 16), (1, 8, 3, 130, 272), (16, 32, 64, 257, 384), (7, 5, 100, 96, 1040),
     (60, 60, 240, 200, 208), (90, 2, 180, 129, 256), (100, 3, 700, 300, 528),
-    (300, 2, 1100, 520, 144), (64, 130, 300, 64, 128)])
+    (300, 2, 1100, 520, 144), (64, 130, 300, 64, 128), (90, 60, 700, 200, 8336),
+    (500, 3, 700, 300, 1168), (800, 2, 2000, 1000, 272), (900, 4, 3000, 2000, 400),
+    (2000, 8, 9000, 2100, 144)])
 @pytest.mark.parametrize("gather", [True, False])
 def test_grouped(dev, T, E, R, N, K, gather, dtype):
     rng = np.random.default_rng(T + E + R)
@@ -74,7 +80,7 @@ def test_grouped(dev, T, E, R, N, K, gather, dtype):
     X, XS, W, WS, off = on(dev, x, xs, w, ws, offsets)
     got = pkg.w8a8_gemm_grouped(X, XS, on(dev, index)[0] if gather else None, off, W, WS,
                                 dtype=TYPES[dtype])
-    close(got, want, ref.bound(mag, want, K, dtype, window(R, E, N, K, dtype)), f"{T} {E} {R}")
+    close(got, want, ref.bound(mag, want, K, dtype, window(R, E, dtype)), f"{T} {E} {R}")
 
 
 # rows per expert: the kernels on both sides of their choice

@@ -121,10 +121,11 @@ def test_products_past_the_grid(lib):
 
 
 def test_kernel_choice(lib):
-    assert lib.w8a8_kernel(1, 1, 4096, 7168, 2) == pkg.W8A8_KERNEL_SKINNY
-    assert lib.w8a8_kernel(4096, 1, 4096, 7168, 2) == pkg.W8A8_KERNEL_TILE
-    for bad in ((0, 1, 64, 64, 0), (1, 0, 64, 64, 0), (1, 1, 0, 64, 0), (1, 1, 64, 40, 0),
-                (1, 1, 64, 64, 3), (BIG, 1, 64, 64, 0), (1, 65536, 64, 64, 0)):
+    for R, E, tile in ((1, 0, False), (4, 0, False), (5, 0, True), (4096, 0, True), (1, 1, False),
+                       (10, 1, False), (11, 1, True), (64, 32, False), (320, 32, False),
+                       (321, 32, True), (3, 65535, False)):
+        assert pkg.w8a8_kernel(R, E) == (pkg.W8A8_KERNEL_TILE if tile else pkg.W8A8_KERNEL_SKINNY)
+    for bad in ((0, 0), (-1, 1), (1, -1), (BIG, 0), (1, 65536)):
         assert lib.w8a8_kernel(*bad) == 0
 
 
