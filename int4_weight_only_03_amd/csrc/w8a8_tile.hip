@@ -239,12 +239,12 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
              wscale0 + ((p >> 6 & 1) * kWB + wave) * 256);
   };
 
-  // operand reads: row 16 u + c of the wave's slots, chunks R and 4 + R
+  // operand reads: the wave's slots 16 (GU u + wu) + c, chunks R and 4 + R
   uint32_t read[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) read[q] = uint32_t(c * 128 + 16 * ((4 * q + R) ^ ((c >> 1) & 7)));
-  const uint32_t xread = uint32_t(16 * WU * wu) * 128, wread = kX + uint32_t(16 * WT * wt) * 128;
-  const int sread = 16 * WU * wu + c;
+  const uint32_t xread = uint32_t(16 * wu) * 128, wread = kX + uint32_t(16 * WT * wt) * 128;
+  const int sread = 16 * wu + c;
 
   constexpr int kDelay = 2;
   f32x4 acc[WU][WT];
@@ -256,14 +256,15 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
   // The products of stage p, and, between them, the copies of stage p + 1 (all at once they
   // would hold up the wave for as long as the memory pipeline takes them).  The FMAs of a sum
   // stand kDelay products behind it; slots are fetched kAhead steps of WT products ahead.
-  constexpr int kAhead = WU > 1 ? 2 : 1, kN = WU * WT, kIssue = kN / 2;
   u32x4m wraw[WT][2];
   auto fetch_w = [&](int t, int p) {
     const unsigned char *img = mem + image_of(p) * kImage + wread + 2048 * t;
     wraw[t][0] = *reinterpret_cast<const u32x4m *>(img + read[0]);
     wraw[t][1] = *reinterpret_cast<const u32x4m *>(img + read[1]);
   };
-  auto multiply = [&](int p) {
+  auto multiply = [&](auto active, int p) {
+    constexpr int A = decltype(active)::value;
+    constexpr int kAhead = A > 1 && A < 8 ? 2 : 1, kN = A * WT, kIssue = kN / 2;
     const unsigned char *img = mem + image_of(p) * kImage;
     // behind the last stage it is copied once more, into images that nobody reads again
     const uint32_t xoff = offset_of(p + (S - 1) * G), woff = offset_of(p + S * G);
@@ -275,9 +276,9 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
     f32x4 d[kDelay];
     float f[kAhead + 1], g = 0.0f;
     auto fetch = [&](int u) {
-      x[u % (kAhead + 1)].set(*reinterpret_cast<const u32x4m *>(img + xread + 2048 * u + read[0]),
-                              *reinterpret_cast<const u32x4m *>(img + xread + 2048 * u + read[1]));
-      f[u % (kAhead + 1)] = s[16 * u];
+      x[u % (kAhead + 1)].set(*reinterpret_cast<const u32x4m *>(img + xread + 2048 * GU * u + read[0]),
+                              *reinterpret_cast<const u32x4m *>(img + xread + 2048 * GU * u + read[1]));
+      f[u % (kAhead + 1)] = s[16 * GU * u];
     };
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) fetch(u);
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
         asm volatile("" : "+v"(acc[v][o]));
       }
       if (i < kN) d[i % kDelay] = now;
-      if (i < kN && t == kDelay - 1 && u + kAhead < WU) fetch(u + kAhead);
+      if (i < kN && t == kDelay - 1 && u + kAhead < A) fetch(u + kAhead);
 #pragma unroll
       for (int j = 0; j < kXC + kWC; ++j) {
         if (j * kIssue / (kXC + kWC) != i) continue;
@@ -340,18 +341,27 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
   for (int t = 0; t < WT; ++t) fetch_w(t, kg);
   // the first stage in which a block may be short
   const int last = a.K % kBlock8 ? a.KB - 2 * G : a.KB;
-  for (int q = 0; q < a.KB; q += G) {
-    const int p = q + kg;  // the group's block
-    landed(std::integral_constant<int, S - 2>());
-    if (q >= last) {
-      clear_behind(p, 0, kXC);
-      clear_behind(p + G, kX, kWC);
+  auto stages = [&](auto active) {
+    for (int q = 0; q < a.KB; q += G) {
+      const int p = q + kg;  // the group's block
+      landed(std::integral_constant<int, S - 2>());
+      if (q >= last) {
+        clear_behind(p, 0, kXC);
+        clear_behind(p + G, kX, kWC);
+      }
+      t8_wait_lds();
+      t8_barrier();
+      if ((q & 63) == 0 && q + 64 < a.KB) copy_wscales(q + 64);
+      if (p < a.KB) multiply(active, p);
     }
-    t8_wait_lds();
-    t8_barrier();
-    if ((q & 63) == 0 && q + 64 < a.KB) copy_wscales(q + 64);
-    if (p < a.KB) multiply(p);
-  }
+  };
+  // a tile that is half full, or less, does half the products
+  if (WU >= 4 && rows <= TM / 4)
+    stages(std::integral_constant<int, WU >= 4 ? WU / 4 : WU>());
+  else if (WU >= 4 && rows <= TM / 2)
+    stages(std::integral_constant<int, WU >= 4 ? WU / 2 : WU>());
+  else
+    stages(std::integral_constant<int, WU>());
   t8_wait_copies<0>();  // the LDS is the next workgroup's, or the sums'
 
   if constexpr (G > 1) {
@@ -384,7 +394,7 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
   OT *y = static_cast<OT *>(a.Y);
 #pragma unroll
   for (int u = 0; u < WU; ++u) {
-    const int m = 16 * WU * wu + 16 * u + c;
+    const int m = 16 * (GU * u + wu) + c;
     if (m >= rows || u % G != kg) continue;
     const int n = n0 + 16 * WT * wt + 4 * WT * R;
     OT *to = y + long(row0 + m) * a.N + n;
