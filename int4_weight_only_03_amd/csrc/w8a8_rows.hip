@@ -6,12 +6,25 @@
 // its largest magnitude is four DPP steps away, no LDS, no barrier.
 
 #include "w8a8_common.h"
-#include "gemv_common.h"
 
 #include <algorithm>
 
 namespace w4a16 {
 namespace {
+
+// silu(g) * u = g / (1 + exp(-g)) * u.  exp(x) = 2^(x log2 e): the exponent's rounding (up to
+// 2^-17 absolute) is taken out again to first order.  v_exp_f32 and v_rcp_f32 are within one
+// unit of 2^-23, so the result is within 6 of them; the compiler's expf and division, a
+// little closer, made the kernel bound by VALU (32768 x 2 x 2048 in bf16: 80 us).
+__device__ __forceinline__ float silu_fast(float g, float u) {
+  constexpr float kHigh = 0x1.715476p+0f, kLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
+  const float p = g * -kHigh;
+  const float e = fmaf(g, -kLow, fmaf(g, -kHigh, -p));
+  const float x = __builtin_amdgcn_exp2f(p);
+  // where x is nothing beside 1, or near infinity, the correction is NaN or idle
+  const float d = 1.0f + (x > 0x1p-100f && x < 0x1p126f ? fmaf(x * e, kLn2, x) : x);
+  return g * __builtin_amdgcn_rcpf(d) * u;
+}
 
 constexpr int kRowsThreads = 256;
 constexpr int kRowsGroups = kRowsThreads / kLanes8;
@@ -37,7 +50,7 @@ quantize_rows(const XT *__restrict__ X, const int32_t *__restrict__ num_rows,
         load8(X + row * (2 * long(K)) + k, v);
         load8(X + row * (2 * long(K)) + K + k, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = silu_mul(v[i], u[i]);
+        for (int i = 0; i < 8; ++i) v[i] = silu_fast(v[i], u[i]);
       } else {
         load8(X + row * K + k, v);
       }

@@ -28,8 +28,9 @@ def check(r, v, dv):
     ref.check_rows(bytes_of(r.codes), r.scales.cpu().numpy(), v, dv)
 
 
-# expf within 2 units, the sum, the quotient and the product: 6 roundings of a unit, and
-# what underflows (expf past fp32's range: the gate counts as 0)
+# the exponential and the reciprocal within a unit of 2^-23 each, the exponent's correction,
+# the sum and two products: 6 units at most, and what underflows (where the exponential
+# leaves fp32's range the gate counts as 0)
 def swiglu_error(x, v):
     u = np.abs(np.asarray(x, np.float64)[:, x.shape[1] // 2:])
     return 6 * 2 * U * np.abs(v) + 2.0 ** -118 * u
@@ -83,6 +84,21 @@ def test_rows_behind_num_rows_stay(dev, rows, kept):
     assert same(out.codes[:kept], whole.codes.view(torch.uint8)[:kept])
     assert same(out.scales[:kept], whole.scales[:kept])
     assert torch.all(out.codes[kept:] == 0x55) and torch.all(out.scales[kept:] == 7.0)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_quantize_swiglu_over_the_range(dev, dtype):
+    """Gates from the type's least to its largest, whose exponentials leave fp32's range."""
+    top = np.log2(torch.finfo(TYPES[dtype]).max) - 0.01
+    rng = np.random.default_rng(3)
+    g = np.concatenate([np.linspace(-100, 100, 4001), np.exp2(np.linspace(-30, top, 991)),
+                        -np.exp2(np.linspace(-30, top, 991)), [0.0]])
+    g = np.pad(g, (0, -len(g) % 16)).astype(np.float32)
+    x = rounded(np.stack([np.concatenate([g, rng.uniform(0.5, 1, len(g)) * s])
+                          for s in (1, -1, 2.0 ** -10)]), dtype)
+    r = pkg.w8a8_quantize(typed(dev, x, dtype), swiglu=True)
+    v = ref.swiglu_rows(x)
+    check(r, v, swiglu_error(x, v))
 
 
 def test_quantize_swiglu_of_infinities(dev):
