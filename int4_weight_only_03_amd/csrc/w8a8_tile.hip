@@ -443,7 +443,7 @@ hipError_t run_tile8(const Gemm8 &p, hipStream_t stream) {
   const long items =
       p.expert_offsets ? max_items(p.R, p.E, TM) : (long(p.R) + TM - 1) / TM;
   const long tiles = items * a.tiles_n;
-  if (tiles > kMaxBlocks * 4 / (GU * GT * G)) return hipErrorInvalidConfiguration;
+  if (tiles > kMaxBlocks * 4 / (GU * GT * G) - 8) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((gemm8_tile<WU, WT, GU, GT, G, S, OT, kExact>), dim3(unsigned((tiles + 7) / 8 * 8)),
                      dim3(64 * GU * GT * G), 0, stream, a);
   return hipGetLastError();
