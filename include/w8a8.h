@@ -96,8 +96,8 @@ int w8a8_quantize(const void *X, const int32_t *num_rows, uint8_t *codes, float 
  * scales is NULL, eps is not positive and finite, weight_dtype is another, or an output
  * overlaps an input (H: otherwise than by being it) or another output; W4A16_ERR_SHAPE
  * also for K > W8A8_NORM_MAX_K or rows that would take 2^32 threads or more (64 a row
- * up to K = 2048, 256 up to 8192, 1024 past that); W4A16_ERR_ALIGN for X, residual, weight, H, Y or codes
- * not 16-byte aligned; otherwise as w8a8_quantize.
+ * up to K = 2048, 256 up to 8192, 1024 past that); W4A16_ERR_ALIGN for X, residual,
+ * weight, H, Y or codes not 16-byte aligned; otherwise as w8a8_quantize.
  */
 int w8a8_rms_norm(const void *X, const void *residual, const void *weight, void *H, void *Y,
                   uint8_t *codes, float *scales, int64_t M, int64_t K, float eps, int32_t dtype,

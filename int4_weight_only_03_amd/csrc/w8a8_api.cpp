@@ -160,7 +160,8 @@ int w8a8_rms_norm(const void *X, const void *residual, const void *weight, void 
                   int32_t weight_dtype, void *stream) {
   const int st = rows_extents(M, K, dtype, W8A8_NORM_MAX_K);
   if (st != W4A16_OK) return st;
-  if (!(eps > 0.0f) || std::isinf(eps) || (weight_dtype != dtype && weight_dtype != W4A16_DTYPE_F32))
+  if (!(eps > 0.0f) || std::isinf(eps) ||
+      (weight_dtype != dtype && weight_dtype != W4A16_DTYPE_F32))
     return W4A16_ERR_ARG;
   if (M == 0) return W4A16_OK;
   if (!X || !weight || !codes != !scales || (!H && !Y && !codes)) return W4A16_ERR_ARG;

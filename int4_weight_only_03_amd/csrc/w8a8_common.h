@@ -1,5 +1,5 @@
 // Device code shared by the 8-bit operators: loads of 8 activations, a group of 128's
-// largest magnitude, its scale and codes.
+// largest magnitude, its scale and codes, codes to fp16.
 #pragma once
 
 #include "moe_common.h"
@@ -13,6 +13,15 @@ typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kLanes8 = 16;  // lanes of a group of 128 values, 8 each
+
+// 8 codes to fp16, exactly
+__device__ __forceinline__ half8v widen8(uint32_t lo, uint32_t hi) {
+  const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false),
+               b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true),
+               c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false),
+               d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+  return half8v{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
 
 __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
   const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);

@@ -3,7 +3,8 @@
 //
 // Bound by HBM (x, r read, H, Y, codes written, each once): a row stays in registers,
 // 8 neighbouring values to a lane and vector, so that the 128 values of a scale are in
-// 16 neighbouring lanes; its sum of squares meets in LDS once.
+// 16 neighbouring lanes; its sum of squares meets in LDS once.  4096 x 7168 in bf16 with all
+// outputs: 265 MB in 56.5 us, 4.7 TB/s of the 4.96 that a copy reaches; a single row 3.3 us.
 
 #include "w8a8_common.h"
 #include "gemv_common.h"
@@ -169,7 +170,9 @@ template <typename XT>
 hipError_t run_norm(const NormArgs &a, hipStream_t stream) {
   // few rows: one vector a thread (us with 256 threads of 4 vectors, with 1024 of one; K =
   // 7168, bf16: 1 row 4.9, 3.3; 256 6.5, 4.5; 512 8.6, 7.4; 1024 11.4, 11.5)
-  if (a.M <= 512 && a.K > 256 && a.K <= 8192) return a.K <= 2048 ? run_norm_with<XT, 256, 1>(a, stream) : run_norm_with<XT, 1024, 1>(a, stream);
+  if (a.M <= 512 && a.K > 256 && a.K <= 8192)
+    return a.K <= 2048 ? run_norm_with<XT, 256, 1>(a, stream)
+                       : run_norm_with<XT, 1024, 1>(a, stream);
   if (a.K <= 2048) return run_norm_with<XT, 64, 4>(a, stream);
   if (a.K <= 8192) return run_norm_with<XT, 256, 4>(a, stream);
   return run_norm_with<XT, 1024, 4>(a, stream);

@@ -3,7 +3,8 @@
 //
 // Bound by HBM: 2 or 4 bytes a value read (twice that with swiglu), 1 + 1/32 written.
 // 16 lanes take the 128 values of a scale, 8 each (one 16-byte load of 16-bit values):
-// its largest magnitude is four DPP steps away, no LDS, no barrier.
+// its largest magnitude is four DPP steps away, no LDS, no barrier.  32768 x 2 x 2048 in bf16:
+// 338 MB in 61 us, 5.5 TB/s (a copy reaches 4.96, a stream of reads 6.3).
 
 #include "w8a8_common.h"
 

@@ -1,5 +1,7 @@
 // 8-bit products for few rows: Y[r] = x_r . W_e^T, weights and activations from memory
-// to registers.
+// to registers.  Bound by HBM where there are many experts (64 slots of 32 experts of 4096 x
+// 7168: 940 MB in 155 us, 6.1 TB/s, a stream of reads alone reaches 6.3), by latency for one
+// (4096 x 7168: 29 MB in 7.1 us, 2 of them the launch).
 //
 // Arithmetic: e4m3 codes become fp16, exactly; 16x16x32 fp16 matrix instructions with
 // fp32 accumulation add up a block of 128 features, and one fp32 FMA per output and
@@ -9,7 +11,7 @@
 // Mapping: A is 16 rows of W, B 16 slots, so that a lane's 4 sums are neighbouring
 // outputs of one slot.  Lane (c, R) (c = lane % 16, R = lane / 16) loads 16 bytes at 16 R
 // and at 64 + 16 R of a block of row c of each; any order of k that both operands share
-// gives the same sum.  A wave takes 16 MT slots of one expert by 16 NT rows of W, KW
+// gives the same sum.  A wave takes 16 slots of one expert by 16 NT rows of W, KW
 // waves of a workgroup its blocks in turn; their sums are added in wave order in LDS.
 
 #include "w8a8_common.h"
@@ -30,25 +32,20 @@ struct SkinnyArgs {
   bool vec;  // rows of Y begin and end at 4 outputs
 };
 
-// 8 codes to fp16, exactly
-__device__ __forceinline__ half8v widen(uint32_t lo, uint32_t hi) {
-  const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false),
-               b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true),
-               c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false),
-               d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
-  return half8v{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-}
+constexpr int kSkinnySlots = 16;
+constexpr int kSkinnyAhead = 2;  // blocks of a wave in flight (4: 7.6 us for 7.1, one row)
 
-template <int MT, int NT, int KW, int P, typename OT>
+template <int NT, int KW, typename OT>
 __global__ void __launch_bounds__(64 * KW) gemm8_skinny(SkinnyArgs a) {
-  __shared__ f32x4 part[KW > 1 ? KW : 1][MT * NT][64];
+  constexpr int P = kSkinnyAhead;
+  __shared__ f32x4 part[KW][NT][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, R = lane >> 4;
   const int item = blockIdx.x / unsigned(a.tiles_n), tile = blockIdx.x % unsigned(a.tiles_n);
-  int e = 0, row0 = item * 16 * MT, rows = std::min(16 * MT, a.R - row0);
+  int e = 0, row0 = item * kSkinnySlots, rows = std::min(kSkinnySlots, a.R - row0);
   if (a.offsets) {
-    const ExpertItem it = find_item(a.offsets, a.E, a.R, 16 * MT, item);
+    const ExpertItem it = find_item(a.offsets, a.E, a.R, kSkinnySlots, item);
     if (it.e < 0) return;  // uniform over the workgroup
     e = it.e;
     row0 = it.row0;
@@ -57,83 +54,63 @@ __global__ void __launch_bounds__(64 * KW) gemm8_skinny(SkinnyArgs a) {
   const int n0 = tile * 16 * NT;
   const long K = a.K;
 
-  const uint8_t *wrow[NT], *xrow[MT];
-  const float *xscale[MT];
+  const uint8_t *wrow[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
     wrow[n] = a.W + (long(e) * a.N + std::min(n0 + 16 * n + c, a.N - 1)) * K;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int slot = row0 + std::min(16 * m + c, rows - 1);
-    long row = slot;
-    if (a.token_index) row = std::min(std::max(a.token_index[slot], 0), a.rows_x - 1);
-    xrow[m] = a.X + row * K;
-    xscale[m] = a.xs + row * a.KB;
-  }
+  long row = row0 + std::min(c, rows - 1);
+  if (a.token_index) row = std::min(std::max(a.token_index[row], 0), a.rows_x - 1);
+  const uint8_t *xrow = a.X + row * K;
+  const float *xscale = a.xs + row * a.KB;
   const float *wscale = a.ws + (long(e) * a.NB + n0 / kBlock8) * a.KB;
 
   struct Step {
-    u32x4m w[NT][2], x[MT][2];
-    float s[MT], t;
+    u32x4m w[NT][2], x[2];
+    float s, t;
   };
   auto load = [&](Step &s, int b) {
-    const int k0 = kBlock8 * b + 16 * R, k1 = k0 + 64;
     // behind the row's end its last 16 bytes are read, and zeros taken
-    const int at0 = std::min(k0, a.K - 16), at1 = std::min(k1, a.K - 16);
+    const int at0 = std::min(kBlock8 * b + 16 * R, a.K - 16),
+              at1 = std::min(kBlock8 * b + 16 * R + 64, a.K - 16);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       s.w[n][0] = *reinterpret_cast<const u32x4m *>(wrow[n] + at0);
       s.w[n][1] = *reinterpret_cast<const u32x4m *>(wrow[n] + at1);
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      s.x[m][0] = *reinterpret_cast<const u32x4m *>(xrow[m] + at0);
-      s.x[m][1] = *reinterpret_cast<const u32x4m *>(xrow[m] + at1);
-      s.s[m] = xscale[m][b];
-    }
+    s.x[0] = *reinterpret_cast<const u32x4m *>(xrow + at0);
+    s.x[1] = *reinterpret_cast<const u32x4m *>(xrow + at1);
+    s.s = xscale[b];
     s.t = wscale[b];
   };
-  f32x4 acc[MT][NT];
+  f32x4 acc[NT];
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[m][n] = zero;
+  for (int n = 0; n < NT; ++n) acc[n] = zero;
   auto multiply = [&](Step &s, int b) {
     if (kBlock8 * (b + 1) > a.K) {
       const u32x4m none = {0, 0, 0, 0};
-      const int k0 = kBlock8 * b + 16 * R, k1 = k0 + 64;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        s.w[n][0] = k0 < a.K ? s.w[n][0] : none;
-        s.w[n][1] = k1 < a.K ? s.w[n][1] : none;
-      }
+      for (int h = 0; h < 2; ++h) {
+        if (kBlock8 * b + 16 * R + 64 * h < a.K) continue;
+        s.x[h] = none;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        s.x[m][0] = k0 < a.K ? s.x[m][0] : none;
-        s.x[m][1] = k1 < a.K ? s.x[m][1] : none;
+        for (int n = 0; n < NT; ++n) s.w[n][h] = none;
       }
     }
-    half8v w[NT][4];
+    half8v x[4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int j = 0; j < 4; ++j)
+      x[j] = widen8(s.x[j / 2][2 * (j & 1)], s.x[j / 2][2 * (j & 1) + 1]);
+    const float f = s.s * s.t;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[n][j] = widen(s.w[n][j / 2][2 * (j & 1)], s.w[n][j / 2][2 * (j & 1) + 1]);
+    for (int n = 0; n < NT; ++n) {
+      f32x4 d = zero;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      half8v x[4];
+      for (int j = 0; j < 4; ++j)
+        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+            widen8(s.w[n][j / 2][2 * (j & 1)], s.w[n][j / 2][2 * (j & 1) + 1]), x[j], d, 0, 0, 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = widen(s.x[m][j / 2][2 * (j & 1)], s.x[m][j / 2][2 * (j & 1) + 1]);
-      const float f = s.s[m] * s.t;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        f32x4 d = zero;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[n][j], x[j], d, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][n][i] = fmaf(f, d[i], acc[m][n][i]);
-      }
+      for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(f, d[i], acc[n][i]);
     }
   };
 
@@ -150,44 +127,30 @@ __global__ void __launch_bounds__(64 * KW) gemm8_skinny(SkinnyArgs a) {
     }
   }
 
-  auto store = [&](int m, int n, f32x4 v) {
-    const int i = 16 * m + c, at = n0 + 16 * n + 4 * R;
-    if (i >= rows) return;
-    OT *y = static_cast<OT *>(a.Y) + long(row0 + i) * a.N + at;
-    if (a.vec) {
-      struct alignas(4 * sizeof(OT)) Four {
-        OT v[4];
-      };
-      if (at < a.N)
-        *reinterpret_cast<Four *>(y) =
-            Four{{from_f32<OT>(v[0]), from_f32<OT>(v[1]), from_f32<OT>(v[2]), from_f32<OT>(v[3])}};
-    } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (at + q < a.N) y[q] = from_f32<OT>(v[q]);
-    }
-  };
-  if constexpr (KW == 1) {
+  for (int n = 0; n < NT; ++n) part[wave][n][lane] = acc[n];
+  __syncthreads();
+  if (wave >= NT || c >= rows) return;
+  f32x4 v = part[0][wave][lane];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) store(m, n, acc[m][n]);
+  for (int w = 1; w < KW; ++w) v += part[w][wave][lane];
+  const int at = n0 + 16 * wave + 4 * R;
+  OT *y = static_cast<OT *>(a.Y) + long(row0 + c) * a.N + at;
+  if (a.vec) {
+    struct alignas(4 * sizeof(OT)) Four {
+      OT v[4];
+    };
+    if (at < a.N)
+      *reinterpret_cast<Four *>(y) =
+          Four{{from_f32<OT>(v[0]), from_f32<OT>(v[1]), from_f32<OT>(v[2]), from_f32<OT>(v[3])}};
   } else {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) part[wave][m * NT + n][lane] = acc[m][n];
-    __syncthreads();
-    for (int i = wave; i < MT * NT; i += KW) {
-      f32x4 v = part[0][i][lane];
-#pragma unroll
-      for (int w = 1; w < KW; ++w) v += part[w][i][lane];
-      store(i / NT, i % NT, v);
-    }
+    for (int q = 0; q < 4; ++q)
+      if (at + q < a.N) y[q] = from_f32<OT>(v[q]);
   }
 }
 
-template <int MT, int NT, int KW, int P, typename OT>
+template <int NT, int KW, typename OT>
 hipError_t run_skinny(const Gemm8 &p, hipStream_t stream) {
   SkinnyArgs a;
   a.X = p.X;
@@ -206,10 +169,12 @@ hipError_t run_skinny(const Gemm8 &p, hipStream_t stream) {
   a.NB = blocks8(p.N);
   a.tiles_n = (p.N + 16 * NT - 1) / (16 * NT);
   a.vec = p.N % 4 == 0 && reinterpret_cast<uintptr_t>(p.Y) % (4 * sizeof(OT)) == 0;
-  const long items = p.expert_offsets ? max_items(p.R, p.E, 16 * MT) : (long(p.R) + 16 * MT - 1) / (16 * MT);
+  const long items = p.expert_offsets
+                         ? max_items(p.R, p.E, kSkinnySlots)
+                         : (long(p.R) + kSkinnySlots - 1) / kSkinnySlots;
   const long blocks = items * a.tiles_n;
   if (blocks > kMaxBlocks * 4 / KW) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((gemm8_skinny<MT, NT, KW, P, OT>), dim3(unsigned(blocks)), dim3(64 * KW), 0,
+  hipLaunchKernelGGL((gemm8_skinny<NT, KW, OT>), dim3(unsigned(blocks)), dim3(64 * KW), 0,
                      stream, a);
   return hipGetLastError();
 }
@@ -219,8 +184,8 @@ hipError_t run_skinny_type(const Gemm8 &p, hipStream_t stream) {
   // Waves of a tile and rows of W by whether the workgroups are many (us with 8 waves and 16
   // rows, 4 and 32: 1 row of 4096 x 7168 7.1, 10.8; 244 slots of 60 experts of 2080 x 1408
   // 56.8, 36.0; 64 of 32 experts of 4096 x 7168 159, 156).
-  return p.expert_offsets ? run_skinny<1, 2, 4, 2, OT>(p, stream)
-                          : run_skinny<1, 1, 8, 2, OT>(p, stream);
+  return p.expert_offsets ? run_skinny<2, 4, OT>(p, stream)
+                          : run_skinny<1, 8, OT>(p, stream);
 }
 
 }  // namespace

@@ -9,9 +9,25 @@
 // anything that is exact.  fp32 outputs take the codes as fp16, exactly, on the 16x16x32 fp16
 // instructions instead.
 //
-// A workgroup's GU x GT waves take 16 WU slots by 16 WT rows of W each.  Stages of one block
-// of features: rows of 128 bytes, and the slots' scales, come to LDS by direct copies one
-// stage ahead, in two images.
+// A tile is 16 WU GU slots by 16 WT GT rows of W: GU x GT waves take 16 WU slots by 16 WT rows
+// each, in turn, so that a half-full tile's work is spread over them.  G such groups of
+// waves share a tile and take its blocks of features in turn; their sums are added in LDS at
+// the end, in the order of the groups.  A stage is one block for each group.  Rows of 128
+// bytes, and the slots' scales, come to LDS by direct copies into a ring of S stages, S - 1 of
+// them in flight, and one barrier a stage; the rows of W go on to registers while the
+// products before them are still under way, so that their image is free a stage earlier and a
+// stage begins with the fetch of 16 slots.
+//
+// Few tiles are bound by latency: a stage takes 0.4 us whatever is in it (64 x 64, one group,
+// 256 x 4096 x 7168: 19.6 us), so groups and small tiles, which put more of K and more of the
+// card to work, win until the tiles are more than the card (64 x 64 with two groups 17.3; 64
+// rows with 32 x 32 and four 9.9).  The largest are bound by power: 256 x 256 runs 8192 x 8192
+// x 8192 in 489 us, 2.25 PFLOP/s, the matrix units busy for 56% of the cycles at 1.9 GHz (2.4
+// without load); left out, the copies between L2 and LDS would save 18%, the FMAs 5%, operand
+// reads from LDS nothing.  Instructions and FMAs alone, in registers, reach 3.7 PFLOP/s.
+// Tried without gain there: operands 1 to 3 steps ahead, copies at once or spread over the
+// stage, half of the waves half a stage behind the others, scales 4 blocks at a time, 32x32x64
+// instructions (3.3 PFLOP/s in registers).
 //
 // Tiles are dealt so that each XCD works a contiguous run of them (the hardware deals
 // workgroups round-robin over the 8 XCDs); see in_band for their order.
@@ -26,7 +42,6 @@ namespace w4a16 {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef __attribute__((address_space(3))) void t8_lds_void;
 
 struct TileArgs {
@@ -70,14 +85,6 @@ __device__ __forceinline__ void t8_copy4(const float *from, uint32_t lds) {
                :: "v"(from), "s"(lds) : "memory", "m0");
 }
 
-__device__ __forceinline__ half8v t8_widen(uint32_t lo, uint32_t hi) {
-  const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false),
-               b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true),
-               c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false),
-               d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
-  return half8v{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-}
-
 // One block of features of 16 rows: 32 codes to a lane, as they are or in fp16.
 template <bool kExact>
 struct Operand;
@@ -92,10 +99,10 @@ template <>
 struct Operand<true> {
   half8v v[4];
   __device__ __forceinline__ void set(u32x4m a, u32x4m b) {
-    v[0] = t8_widen(a.x, a.y);
-    v[1] = t8_widen(a.z, a.w);
-    v[2] = t8_widen(b.x, b.y);
-    v[3] = t8_widen(b.z, b.w);
+    v[0] = widen8(a.x, a.y);
+    v[1] = widen8(a.z, a.w);
+    v[2] = widen8(b.x, b.y);
+    v[3] = widen8(b.z, b.w);
   }
 };
 __device__ __forceinline__ f32x4 block_sum(const Operand<false> &w, const Operand<false> &x) {
@@ -105,13 +112,15 @@ __device__ __forceinline__ f32x4 block_sum(const Operand<false> &w, const Operan
 __device__ __forceinline__ f32x4 block_sum(const Operand<true> &w, const Operand<true> &x) {
   f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.v[j], x.v[j], d, 0, 0, 0);
+  for (int j = 0; j < 4; ++j)
+    d = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.v[j], x.v[j], d, 0, 0, 0);
   return d;
 }
 
 // Tile `i` of `tiles_m` x `tiles_n`: bands of kBand blocks of slots, in a band the blocks of
 // slots fastest, so that the 32 tiles that an XCD holds at once are about 4 x 8 and share
-// their operands in its L2.
+// their operands in its L2 (8192 x 8192 x 8192: 556 us with all of an expert's blocks of slots
+// fastest, 494 so; 4 and 8 of them alike).
 constexpr int kBand = 4;
 __device__ __forceinline__ void in_band(long i, int tiles_m, int tiles_n, int &bm, int &bn) {
   const long band = i / (long(kBand) * tiles_n);
@@ -122,7 +131,8 @@ __device__ __forceinline__ void in_band(long i, int tiles_m, int tiles_n, int &b
 }
 
 template <int WU, int WT, int GU, int GT, int G, int S, typename OT, bool kExact>
-__global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * GT / 4 : 2) gemm8_tile(TileArgs a) {
+__global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * GT / 4 : 2)
+gemm8_tile(TileArgs a) {
   constexpr int kWaves = GU * GT;  // of a group
   constexpr int TM = 16 * WU * GU, TN = 16 * WT * GT;  // slots and rows of W of a tile
   constexpr int kX = TM * 128, kImage = kX + TN * 128;
@@ -142,8 +152,7 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
   const int c = lane & 15, R = lane >> 4;
   const int wu = wave % GU, wt = wave / GU;
 
-  // tile of this workgroup: XCD b % 8 takes a contiguous run of the tiles there are; within
-  // an expert its blocks of slots are fastest
+  // tile of this workgroup: XCD b % 8 takes a contiguous run of the tiles there are
   int e = 0, bm, bn, e0 = 0, e1 = a.R;
   {
     const long index = long(blockIdx.x >> 3);
@@ -199,7 +208,9 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
   auto image_of = [&](int p) { return uint32_t(p & (S * G - 1)); };
   // where a lane reads in its rows for block p; behind their end (the last block of K may be
   // shorter than 128) their last 16 bytes once more
-  auto offset_of = [&](int p) { return std::min(uint32_t(p) * kBlock8 + chunk, uint32_t(a.K) - 16); };
+  auto offset_of = [&](int p) {
+    return std::min(uint32_t(p) * kBlock8 + chunk, uint32_t(a.K) - 16);
+  };
   // copy j of block p's slots and of its rows of W
   auto copy_x = [&](int j, int p, uint32_t at) {
     t8_copy16(xat[j] + at, lds0 + image_of(p) * kImage + 1024 * (wave + j * kWaves));
@@ -216,8 +227,9 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
                                   16 * lane) = u32x4m{0, 0, 0, 0};
   };
 
-  // scales: every wave copies those of as many slots (each lane's lies in a cache line of its
-  // own, which costs as much as 16 bytes)
+  // scales: every wave copies those of as many slots, so that every wave has as many copies
+  // in flight (a lane's lies in a cache line of its own: where all waves copied 64 slots' each,
+  // most of them twice, 256 x 256 took 10% longer)
   constexpr int kSC = kS / kWaves;
   const uint32_t scale0 = uint32_t(reinterpret_cast<uintptr_t>((const t8_lds_void *)scale));
   const float *sx = a.xs;
@@ -253,9 +265,10 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
 #pragma unroll
     for (int t = 0; t < WT; ++t) acc[u][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // The products of stage p, and, between them, the copies of stage p + 1 (all at once they
-  // would hold up the wave for as long as the memory pipeline takes them).  The FMAs of a sum
-  // stand kDelay products behind it; slots are fetched kAhead steps of WT products ahead.
+  // The products of block p with the wave's first A tiles of 16 slots, and, between them, the
+  // copies for S - 1 stages on and the fetch of the next block's rows of W.  The FMAs of a sum
+  // stand kDelay products behind it (right behind it they would wait 12 cycles each: 125 us of
+  // 4096 x 4096 x 7168 then, 114 so); slots are fetched kAhead steps of WT products ahead.
   u32x4m wraw[WT][2];
   auto fetch_w = [&](int t, int p) {
     const unsigned char *img = mem + image_of(p) * kImage + wread + 2048 * t;
@@ -266,7 +279,8 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
     constexpr int A = decltype(active)::value;
     constexpr int kAhead = A > 1 && A < 8 ? 2 : 1, kN = A * WT, kIssue = kN / 2;
     const unsigned char *img = mem + image_of(p) * kImage;
-    // behind the last stage it is copied once more, into images that nobody reads again
+    // behind the last block it is copied once more, into images that nobody reads again:
+    // without a condition every wave has as many copies in flight
     const uint32_t xoff = offset_of(p + (S - 1) * G), woff = offset_of(p + S * G);
     const float *s = scale + int(image_of(p)) * kS + sread;
     const float fw = wscale[((p >> 6 & 1) * kWB + 16 * WT * wt / kBlock8) * 64 + (p & 63)];
@@ -276,8 +290,9 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
     f32x4 d[kDelay];
     float f[kAhead + 1], g = 0.0f;
     auto fetch = [&](int u) {
-      x[u % (kAhead + 1)].set(*reinterpret_cast<const u32x4m *>(img + xread + 2048 * GU * u + read[0]),
-                              *reinterpret_cast<const u32x4m *>(img + xread + 2048 * GU * u + read[1]));
+      const unsigned char *at = img + xread + 2048 * GU * u;
+      x[u % (kAhead + 1)].set(*reinterpret_cast<const u32x4m *>(at + read[0]),
+                              *reinterpret_cast<const u32x4m *>(at + read[1]));
       f[u % (kAhead + 1)] = s[16 * GU * u];
     };
 #pragma unroll
@@ -355,7 +370,8 @@ __global__ void __launch_bounds__(64 * GU * GT * G, G * GU * GT > 8 ? G * GU * G
       if (p < a.KB) multiply(active, p);
     }
   };
-  // a tile that is half full, or less, does half the products
+  // A tile that is half full, or less, does half the products (4096 tokens, 4 of 32 experts of
+  // 4096 x 7168: 628 us without, 595 so).
   if (WU >= 4 && rows <= TM / 4)
     stages(std::integral_constant<int, WU >= 4 ? WU / 4 : WU>());
   else if (WU >= 4 && rows <= TM / 2)
@@ -444,8 +460,8 @@ hipError_t run_tile8(const Gemm8 &p, hipStream_t stream) {
       p.expert_offsets ? max_items(p.R, p.E, TM) : (long(p.R) + TM - 1) / TM;
   const long tiles = items * a.tiles_n;
   if (tiles > kMaxBlocks * 4 / (GU * GT * G) - 8) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((gemm8_tile<WU, WT, GU, GT, G, S, OT, kExact>), dim3(unsigned((tiles + 7) / 8 * 8)),
-                     dim3(64 * GU * GT * G), 0, stream, a);
+  hipLaunchKernelGGL((gemm8_tile<WU, WT, GU, GT, G, S, OT, kExact>),
+                     dim3(unsigned((tiles + 7) / 8 * 8)), dim3(64 * GU * GT * G), 0, stream, a);
   return hipGetLastError();
 }
 
