@@ -487,37 +487,67 @@ constexpr Choice kExactChoices[] = {  // fp32 outputs: no more registers for lar
     {64, 64, 1, 23.5, 23.5},  {64, 64, 2, 31.3, 40.0},  {128, 128, 2, 66.0, 110.0},
 };
 
-// The choice of least time: rounds of tiles over 256 compute units.  An expert's last tile
-// is on the average half empty, and one of 128 slots or more that is takes less time (32
-// experts of 4096 x 7168, bf16, us with 128 and 256 slots: mean 64 197, 206; 94 268, 217; 128
-// 273, 239; 188 343, 340; 256 404, 351).
-template <int kCount>
-int least(const Choice (&list)[kCount], const Gemm8 &p) {
+// Time of a choice: rounds of tiles over 256 compute units.  An expert's last tile is on the
+// average half empty, and one of 128 slots or more that is takes less time (32 experts of 4096
+// x 7168, bf16, us with 128 and 256 slots: mean 64 197, 206; 94 268, 217; 128 273, 239; 188
+// 343, 340; 256 404, 351).
+double time_of(const Choice &c, const Gemm8 &p, long R) {
   const double experts = p.expert_offsets ? std::min(p.R, p.E) : 1;
-  int best = 0;
-  double least = 0.0;
-  for (int i = 0; i < kCount; ++i) {
-    const Choice &c = list[i];
-    const double items = p.expert_offsets
-                             ? experts * std::max(1.0, p.R / experts / c.slots + 0.5)
-                             : double((long(p.R) + c.slots - 1) / c.slots);
-    const double tiles = items * double((long(p.N) + c.rows - 1) / c.rows);
-    const double rounds = std::floor(tiles / (256 * c.per_cu));
-    const double rest = tiles - rounds * 256 * c.per_cu;
-    double t = rounds * c.all + (rest <= 0.0 ? 0.0 : rest <= 256.0 ? c.one : c.all);
-    if (p.expert_offsets && c.slots >= 128)
-      t *= 0.5 + 0.5 * std::min(1.0, p.R / experts / c.slots);
-    if (i == 0 || t < least) {
-      least = t;
-      best = i;
-    }
+  const double items = p.expert_offsets ? experts * std::max(1.0, R / experts / c.slots + 0.5)
+                                        : double((R + c.slots - 1) / c.slots);
+  const double tiles = items * double((long(p.N) + c.rows - 1) / c.rows);
+  const double rounds = std::floor(tiles / (256 * c.per_cu));
+  const double rest = tiles - rounds * 256 * c.per_cu;
+  // A round that leaves half of the card idle is up to a fifth faster (256 x 256: 64 tiles 80,
+  // 128 82, 168 83, 256 103).
+  const double part = rest <= 256.0 ? c.one * (0.8 + 0.2 * std::max(0.0, rest / 128 - 1.0)) : c.all;
+  const double t = rounds * c.all + (rest > 0.0 ? part : 0.0);
+  return p.expert_offsets && c.slots >= 128
+             ? t * (0.5 + 0.5 * std::min(1.0, R / experts / c.slots))
+             : t;
+}
+
+struct Best {
+  int choice;
+  double time;
+};
+template <int kCount>
+Best least(const Choice (&list)[kCount], const Gemm8 &p, long R) {
+  Best best = {0, time_of(list[0], p, R)};
+  for (int i = 1; i < kCount; ++i) {
+    const double t = time_of(list[i], p, R);
+    if (t < best.time) best = {i, t};
   }
   return best;
 }
 
+// Rows of X that one launch takes, whole rounds of its tiles, before another takes the rest
+// (all of them: one launch is the best).  Only where a round is worth it beside a launch (2
+// us) and the host's own time.  us with one launch and with two, bf16: 1030 x 4096 x 7168 56,
+// 45; 4100 165, 112; fp32 101, 80.
+template <int kCount>
+long rows_before_rest(const Choice (&list)[kCount], const Gemm8 &p) {
+  const double blocks = blocks8(p.K) / 56.0;
+  double least_time = least(list, p, p.R).time;
+  long rows = p.R;
+  if (p.expert_offsets || least_time * blocks < 25.0) return rows;
+  for (const Choice &c : list) {
+    const long tiles_n = (long(p.N) + c.rows - 1) / c.rows, round = 256L * c.per_cu;
+    const long tiles = (long(p.R) + c.slots - 1) / c.slots * tiles_n;
+    const long first = tiles / round * round / tiles_n * c.slots;
+    if (first <= 0 || first >= p.R) continue;
+    const double t = least(list, p, first).time + least(list, p, p.R - first).time + 2.0 / blocks;
+    if (t < least_time) {
+      least_time = t;
+      rows = first;
+    }
+  }
+  return rows;
+}
+
 template <typename OT>
 hipError_t run_type8(const Gemm8 &p, hipStream_t stream) {
-  switch (least(kChoices, p)) {
+  switch (least(kChoices, p, p.R).choice) {
     case 0: return run_tile8<1, 1, 1, 2, 4, 4, OT, false>(p, stream);
     case 1: return run_tile8<1, 1, 2, 2, 4, 4, OT, false>(p, stream);
     case 2: return run_tile8<1, 2, 2, 2, 2, 4, OT, false>(p, stream);
@@ -531,7 +561,7 @@ hipError_t run_type8(const Gemm8 &p, hipStream_t stream) {
 }
 
 hipError_t run_exact8(const Gemm8 &p, hipStream_t stream) {
-  switch (least(kExactChoices, p)) {
+  switch (least(kExactChoices, p, p.R).choice) {
     case 0: return run_tile8<1, 1, 1, 2, 4, 4, float, true>(p, stream);
     case 1: return run_tile8<1, 1, 2, 2, 4, 4, float, true>(p, stream);
     case 2: return run_tile8<1, 2, 2, 2, 2, 4, float, true>(p, stream);
@@ -558,11 +588,25 @@ hipError_t launch_gemm8(const Gemm8 &p, hipStream_t stream) {
 }
 
 hipError_t launch_gemm8_tile(const Gemm8 &p, hipStream_t stream) {
-  switch (p.dtype) {
-    case W4A16_DTYPE_F32: return run_exact8(p, stream);
-    case W4A16_DTYPE_F16: return run_type8<_Float16>(p, stream);
-    default: return run_type8<Bf16>(p, stream);
-  }
+  auto run = [&](const Gemm8 &part) {
+    switch (p.dtype) {
+      case W4A16_DTYPE_F32: return run_exact8(part, stream);
+      case W4A16_DTYPE_F16: return run_type8<_Float16>(part, stream);
+      default: return run_type8<Bf16>(part, stream);
+    }
+  };
+  const bool exact = p.dtype == W4A16_DTYPE_F32;
+  const long rows = exact ? rows_before_rest(kExactChoices, p) : rows_before_rest(kChoices, p);
+  Gemm8 part = p;
+  part.R = part.rows_x = int(rows);
+  if (p.expert_offsets) part.rows_x = p.rows_x;
+  const hipError_t e = run(part);
+  if (e != hipSuccess || rows >= p.R) return e;
+  part.R = part.rows_x = int(p.R - rows);
+  part.X += rows * p.K;
+  part.xs += rows * blocks8(p.K);
+  part.Y = static_cast<unsigned char *>(p.Y) + rows * p.N * (exact ? 4 : 2);
+  return run(part);
 }
 
 }  // namespace w4a16

@@ -74,6 +74,31 @@ def test_outputs_past_2_32_bytes(dev):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("M,N,K", [(1030, 4096, 7168), (4100, 4100, 3600), (3000, 7168, 2048)])
+def test_rows_behind_whole_rounds(dev, M, N, K, dtype):
+    """Sizes whose last rows a launch of their own may take."""
+    table = torch.from_numpy(np.nan_to_num(ref.E4M3)).to(dev)
+    X, W = random_codes(dev, M, K), random_codes(dev, N, K)
+    xs = torch.rand(M, ref.blocks(K), device=dev) * 2.0 ** -10
+    ws = torch.rand(ref.blocks(N), ref.blocks(K), device=dev) * 2.0 ** -10
+
+    def wide(scales):
+        return scales.double().repeat_interleave(128, -1)[..., :K]
+
+    x = table[X.long()] * wide(xs)
+    w = table[W.long()] * wide(ws).repeat_interleave(128, 0)[:N]
+    want, mag = x @ w.t(), x.abs() @ w.abs().t()
+    got = pkg.w8a8_gemm(X, xs, W, ws, dtype=TYPES[dtype])
+    tol = (2 * 128 + ref.blocks(K) + 4) * ref.U * mag
+    if dtype != "fp32":
+        tol += ref.WINDOW * mag
+    tol += ref.HALF_STEP[dtype] * (want.abs() + tol) + ref.SMALLEST[dtype]
+    err = (got.double() - want).abs()
+    print(f"  max err/bound {(err / tol).max().item():.3e}", flush=True)
+    assert bool((err <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("M", [1, 30, 130])
 def test_longest_rows(dev, M, dtype):
     rng = np.random.default_rng(M)
