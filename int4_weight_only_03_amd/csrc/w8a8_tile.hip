@@ -27,7 +27,10 @@
 // reads from LDS nothing.  Instructions and FMAs alone, in registers, reach 3.7 PFLOP/s.
 // Tried without gain there: operands 1 to 3 steps ahead, copies at once or spread over the
 // stage, half of the waves half a stage behind the others, scales 4 blocks at a time, 32x32x64
-// instructions (3.3 PFLOP/s in registers).
+// instructions (3.3 PFLOP/s in registers).  By expert (16384 slots of 32 experts of 4096 x 7168,
+// shares from half to one and a half times the mean): part-filled tiles behind all the others
+// 578 us for 537, as they read their weights once more, all at one time; XCDs' runs cut by
+// cost, a half-full tile as half of one, 611 for 550, as their weights take it as long.
 //
 // Tiles are dealt so that each XCD works a contiguous run of them (the hardware deals
 // workgroups round-robin over the 8 XCDs); see in_band for their order.

@@ -98,6 +98,31 @@ def test_rows_behind_whole_rounds(dev, M, N, K, dtype):
     assert bool((err <= tol).all())
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_whole_rounds_and_rest_in_a_graph(dev, dtype):
+    """Such a product captured, on inputs that change: bit for bit the eager one's, and nothing
+    of the rows around its output is touched."""
+    M, N, K = 1030, 4096, 7168
+    W = random_codes(dev, N, K)
+    X, xs = random_codes(dev, M, K), torch.rand(M, ref.blocks(K), device=dev) * 2.0 ** -10
+    ws = torch.rand(ref.blocks(N), ref.blocks(K), device=dev) * 2.0 ** -10
+    around = torch.full((M + 16, N), 7.0, dtype=TYPES[dtype], device=dev)
+    Y = around[8:M + 8]
+    pkg.w8a8_gemm(X, xs, W, ws, Y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkg.w8a8_gemm(X, xs, W, ws, Y)
+    for _ in range(3):
+        X.copy_(random_codes(dev, M, K))
+        xs.copy_(torch.rand_like(xs) * 2.0 ** -10)
+        Y.fill_(7.0)
+        graph.replay()
+        got = Y.clone()
+        assert same(got, pkg.w8a8_gemm(X, xs, W, ws, dtype=TYPES[dtype]))
+    assert bool((around[:8] == 7).all()) and bool((around[M + 8:] == 7).all())
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("M", [1, 30, 130])
 def test_longest_rows(dev, M, dtype):
