@@ -30,7 +30,9 @@
 // instructions (3.3 PFLOP/s in registers).  By expert (16384 slots of 32 experts of 4096 x 7168,
 // shares from half to one and a half times the mean): part-filled tiles behind all the others
 // 578 us for 537, as they read their weights once more, all at one time; XCDs' runs cut by
-// cost, a half-full tile as half of one, 611 for 550, as their weights take it as long.
+// cost, a half-full tile as half of one, 611 for 550; to every XCD an eighth of every expert's
+// tiles 563 for 555.  What stands idle leaves power to the others, so what counts is the
+// products that padding adds, not how evenly they are dealt.
 //
 // Tiles are dealt so that each XCD works a contiguous run of them (the hardware deals
 // workgroups round-robin over the 8 XCDs); see in_band for their order.
@@ -280,7 +282,7 @@ gemm8_tile(TileArgs a) {
   };
   auto multiply = [&](auto active, int p) {
     constexpr int A = decltype(active)::value;
-    constexpr int kAhead = A > 1 && A < 8 ? 2 : 1, kN = A * WT, kIssue = kN / 2;
+    constexpr int kAhead = A > 1 && A < 6 ? 2 : 1, kN = A * WT, kIssue = kN / 2;
     const unsigned char *img = mem + image_of(p) * kImage;
     // behind the last block it is copied once more, into images that nobody reads again:
     // without a condition every wave has as many copies in flight
@@ -374,11 +376,14 @@ gemm8_tile(TileArgs a) {
     }
   };
   // A tile that is half full, or less, does half the products (4096 tokens, 4 of 32 experts of
-  // 4096 x 7168: 628 us without, 595 so).
+  // 4096 x 7168: 628 us without, 595 so), a large one that is three quarters full those (16384
+  // slots of such experts with shares from half to one and a half times the mean: 555, 550).
   if (WU >= 4 && rows <= TM / 4)
     stages(std::integral_constant<int, WU >= 4 ? WU / 4 : WU>());
   else if (WU >= 4 && rows <= TM / 2)
     stages(std::integral_constant<int, WU >= 4 ? WU / 2 : WU>());
+  else if (WU >= 8 && rows <= 3 * TM / 4)
+    stages(std::integral_constant<int, WU >= 8 ? 3 * WU / 4 : WU>());
   else
     stages(std::integral_constant<int, WU>());
   t8_wait_copies<0>();  // the LDS is the next workgroup's, or the sums'

@@ -98,6 +98,36 @@ def test_rows_behind_whole_rounds(dev, M, N, K, dtype):
     assert bool((err <= tol).all())
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_part_filled_tiles(dev, dtype):
+    """Experts whose last tiles hold few slots, a quarter, half, three quarters of them and one
+    more, and all but one."""
+    N, K = 4104, 272
+    last = (1, 16, 63, 64, 65, 128, 129, 192, 193, 255)
+    off = np.concatenate([[0], np.cumsum([1024 + n for n in last])]).astype(np.int32)
+    E, R = len(last), int(off[-1])
+    table = torch.from_numpy(np.nan_to_num(ref.E4M3)).to(dev)
+    X, W = random_codes(dev, R, K), random_codes(dev, E, N, K)
+    xs = torch.rand(R, ref.blocks(K), device=dev) * 2.0 ** -10
+    ws = torch.rand(E, ref.blocks(N), ref.blocks(K), device=dev) * 2.0 ** -10
+    got = pkg.w8a8_gemm_grouped(X, xs, None, torch.from_numpy(off).to(dev), W, ws,
+                                dtype=TYPES[dtype])
+    for e in range(E):
+        rows = slice(int(off[e]), int(off[e + 1]))
+        x = table[X[rows].long()] * xs[rows].double().repeat_interleave(128, -1)[:, :K]
+        w = table[W[e].long()] * ws[e].double().repeat_interleave(128, -1)[:, :K] \
+            .repeat_interleave(128, 0)[:N]
+        want, mag = x @ w.t(), x.abs() @ w.abs().t()
+        tol = (2 * 128 + ref.blocks(K) + 4) * ref.U * mag
+        if dtype != "fp32":
+            tol += ref.WINDOW * mag
+        tol += ref.HALF_STEP[dtype] * (want.abs() + tol) + ref.SMALLEST[dtype]
+        err = (got[rows].double() - want).abs()
+        print(f"  {last[e]} behind the last whole tile: max err/bound "
+              f"{(err / tol).max().item():.3e}", flush=True)
+        assert bool((err <= tol).all())
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_whole_rounds_and_rest_in_a_graph(dev, dtype):
     """Such a product captured, on inputs that change: bit for bit the eager one's, and nothing
