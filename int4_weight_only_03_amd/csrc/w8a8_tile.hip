@@ -415,30 +415,68 @@ gemm8_tile(TileArgs a) {
     }
   }
 
-  OT *y = static_cast<OT *>(a.Y);
+  OT *y = static_cast<OT *>(a.Y) + long(row0) * a.N + n0;
+  const int n = 16 * WT * wt + 4 * WT * R, cols = std::min(TN, a.N - n0);  // of the tile
+  if (a.vec) {
+    constexpr int kV = std::min(int(16 / sizeof(OT)), 4 * WT);
+    struct alignas(kV * sizeof(OT)) Some {
+      OT v[kV];
+    };
 #pragma unroll
-  for (int u = 0; u < WU; ++u) {
-    const int m = 16 * (GU * u + wu) + c;
-    if (m >= rows || u % G != kg) continue;
-    const int n = n0 + 16 * WT * wt + 4 * WT * R;
-    OT *to = y + long(row0 + m) * a.N + n;
-    if (a.vec) {
-      constexpr int kV = std::min(int(16 / sizeof(OT)), 4 * WT);
-      struct alignas(kV * sizeof(OT)) Some {
-        OT v[kV];
-      };
+    for (int u = 0; u < WU; ++u) {
+      const int m = 16 * (GU * u + wu) + c;
+      if (m >= rows || u % G != kg) continue;
 #pragma unroll
       for (int v = 0; v < 4 * WT / kV; ++v) {
         Some o;
 #pragma unroll
         for (int i = 0; i < kV; ++i)
           o.v[i] = from_f32<OT>(acc[u][(kV * v + i) / 4][(kV * v + i) % 4]);
-        if (n + kV * v < a.N) *reinterpret_cast<Some *>(to + kV * v) = o;
+        if (n + kV * v < cols) *reinterpret_cast<Some *>(y + long(m) * a.N + n + kV * v) = o;
       }
-    } else {
+    }
+    return;
+  }
+  // Rows that begin anywhere: to LDS first, each row as far behind a multiple of 16 bytes as
+  // in memory, so that whole 16 bytes of it are read and stored (4096 x 4095 x 7168, bf16: 144
+  // us with single outputs stored from the sums).
+  constexpr int kV = 16 / sizeof(OT), kPitch = TN + kV, kChunks = TN / kV + 1;
+  constexpr int kPart = WU * 16 * GU * kPitch * sizeof(OT) <= sizeof(mem) ? WU : WU / 2;
+  static_assert(kPart * 16 * GU * kPitch * sizeof(OT) <= sizeof(mem), "room for the outputs");
+  OT *const out = reinterpret_cast<OT *>(mem);
+  auto behind = [&](int m) {
+    return int((reinterpret_cast<uintptr_t>(y + long(m) * a.N) & 15) / sizeof(OT));
+  };
 #pragma unroll
-      for (int i = 0; i < 4 * WT; ++i)
-        if (n + i < a.N) to[i] = from_f32<OT>(acc[u][i / 4][i % 4]);
+  for (int u0 = 0; u0 < WU; u0 += kPart) {
+    t8_wait_lds();
+    t8_barrier();  // nobody reads what is there any more
+    const int m0 = 16 * GU * u0, m1 = std::min(rows, m0 + 16 * GU * kPart);
+#pragma unroll
+    for (int u = u0; u < u0 + kPart; ++u) {
+      const int m = 16 * (GU * u + wu) + c;
+      if (m >= rows || u % G != kg) continue;
+      OT *to = out + (m - m0) * kPitch + behind(m) + n;
+#pragma unroll
+      for (int i = 0; i < 4 * WT; ++i) to[i] = from_f32<OT>(acc[u][i / 4][i % 4]);
+    }
+    t8_wait_lds();
+    t8_barrier();
+    for (int i = tid; i < (m1 - m0) * kChunks; i += 64 * kWaves * G) {
+      const int m = m0 + i / kChunks, at = kV * (i % kChunks);
+      struct alignas(16) Chunk {
+        OT v[kV];
+      };
+      const Chunk o = *reinterpret_cast<const Chunk *>(out + (m - m0) * kPitch + at);
+      const int first = at - behind(m);  // column
+      OT *to = y + long(m) * a.N + first;
+      if (first >= 0 && first + kV <= cols) {
+        *reinterpret_cast<Chunk *>(to) = o;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kV; ++j)
+          if (first + j >= 0 && first + j < cols) to[j] = o.v[j];
+      }
     }
   }
 }

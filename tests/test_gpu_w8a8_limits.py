@@ -128,6 +128,27 @@ def test_part_filled_tiles(dev, dtype):
         assert bool((err <= tol).all())
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("M,N", [(20, 4097), (64, 7169), (130, 4099), (300, 4103), (900, 4101),
+                                 (2049, 4095), (4097, 4111)])
+def test_odd_rows_of_outputs(dev, M, N, dtype):
+    """Outputs whose rows begin anywhere, at any start: bit for bit those of whole vectors (the
+    same product with rows of W more), and nothing around them is touched."""
+    K = 400
+    X, W = random_codes(dev, M, K), random_codes(dev, N, K)
+    xs = torch.rand(M, ref.blocks(K), device=dev) * 2.0 ** -10
+    ws = torch.rand(ref.blocks(N), ref.blocks(K), device=dev) * 2.0 ** -10
+    more = -N % 8  # in N's last block, or the 8 rows would need scales of their own
+    want = pkg.w8a8_gemm(X, xs, torch.cat([W, W[:more]]), ws if ref.blocks(N + more) == len(ws)
+                         else torch.cat([ws, ws[:1]]), dtype=TYPES[dtype])[:, :N]
+    for at in (0, 1, 5):
+        room = torch.full((M * N + 32,), 7.0, dtype=TYPES[dtype], device=dev)
+        Y = room[at + 8:at + 8 + M * N].view(M, N)
+        pkg.w8a8_gemm(X, xs, W, ws, Y)
+        assert same(Y, want.contiguous())
+        assert bool((room[:at + 8] == 7).all()) and bool((room[at + 8 + M * N:] == 7).all())
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_whole_rounds_and_rest_in_a_graph(dev, dtype):
     """Such a product captured, on inputs that change: bit for bit the eager one's, and nothing
