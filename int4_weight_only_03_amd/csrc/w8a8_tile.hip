@@ -20,9 +20,9 @@
 //
 // Few tiles are bound by latency: a stage takes 0.4 us whatever is in it (64 x 64, one group,
 // 256 x 4096 x 7168: 19.6 us), so groups and small tiles, which put more of K and more of the
-// card to work, win until the tiles are more than the card (64 x 64 with two groups 17.3; 64
-// rows with 32 x 32 and four 9.9).  The largest are bound by power: 256 x 256 runs 8192 x 8192
-// x 8192 in 489 us, 2.25 PFLOP/s, the matrix units busy for 56% of the cycles at 1.9 GHz (2.4
+// card to work, win until the tiles are more than the card (64 x 64 with two groups 17.1; 64
+// rows with 32 x 32 and four 10.4).  The largest are bound by power: 256 x 256 runs 8192 x 8192
+// x 8192 in 464 us, 2.37 PFLOP/s, the matrix units busy for 56% of the cycles at 1.9 GHz (2.4
 // without load); left out, the copies between L2 and LDS would save 18%, the FMAs 5%, operand
 // reads from LDS nothing.  Instructions and FMAs alone, in registers, reach 3.7 PFLOP/s.
 // Tried without gain there: operands 1 to 3 steps ahead, copies at once or spread over the
@@ -417,7 +417,12 @@ gemm8_tile(TileArgs a) {
 
   OT *y = static_cast<OT *>(a.Y) + long(row0) * a.N + n0;
   const int n = 16 * WT * wt + 4 * WT * R, cols = std::min(TN, a.N - n0);  // of the tile
-  if (a.vec) {
+  // Whole vectors straight from the sums, where they are a good part of a cache line: of fp32
+  // in tiles of 128 rows a lane's 16 outputs take four stores, each to 64 places, and the way
+  // through LDS below is the faster (4096 x 4096 x 1024: 51.6 us, 45.7 so; 64 x 64 tiles and
+  // 16-bit outputs lose by it: 500 x 1408 x 2064 11.9, 12.3; 4096 x 4096 x 1024 in bf16 22.5,
+  // 26.2).
+  if (a.vec && (sizeof(OT) == 2 || WT < 4)) {
     constexpr int kV = std::min(int(16 / sizeof(OT)), 4 * WT);
     struct alignas(kV * sizeof(OT)) Some {
       OT v[kV];
@@ -570,7 +575,7 @@ Best least(const Choice (&list)[kCount], const Gemm8 &p, long R) {
 // Rows of X that one launch takes, whole rounds of its tiles, before another takes the rest
 // (all of them: one launch is the best).  Only where a round is worth it beside a launch (2
 // us) and the host's own time.  us with one launch and with two, bf16: 1030 x 4096 x 7168 56,
-// 45; 4100 165, 112; fp32 101, 80.
+// 44; 4100 165, 106; fp32 101, 80.
 template <int kCount>
 long rows_before_rest(const Choice (&list)[kCount], const Gemm8 &p) {
   const double blocks = blocks8(p.K) / 56.0;
@@ -620,7 +625,7 @@ hipError_t run_exact8(const Gemm8 &p, hipStream_t stream) {
 }  // namespace
 
 // Few rows: the skinny kernel.  Of one expert (4096 rows of W x 7168, us skinny against the
-// tiles): 1 row 7.1, 7.4 (fp32 outputs 9.3), 16 rows 10.5, 7.6; of many by their mean (32 of
+// tiles): 1 row 7.1, 7.4 (fp32 outputs 9.3), 16 rows 10.5, 8.1; of many by their mean (32 of
 // the same): 2 156, 168; 8 167, 182; 16 240, 176.
 int gemm8_kernel(long R, long E, bool grouped) {
   if (!grouped) return R <= 4 ? W8A8_KERNEL_SKINNY : W8A8_KERNEL_TILE;
