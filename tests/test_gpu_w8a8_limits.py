@@ -190,6 +190,31 @@ def test_longest_rows(dev, M, dtype):
     close(got, want, ref.bound(mag, want, K, dtype, window), f"{M} rows")
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (3, 700, 8192), (2, 33, 12288)])
+def test_rows_of_whole_pages(dev, M, N, K, dtype):
+    """Few rows at lengths where workgroups begin at blocks of their own, dense and by expert; a
+    NaN in any block reaches its outputs and no others."""
+    rng = np.random.default_rng(N)
+    E, R = 3, 3 * M
+    x, xs = codes_of(rng, R, K), scales_of(rng, R, K // 128) * np.float32(2.0 ** -12)
+    w, ws = codes_of(rng, E, N, K), scales_of(rng, E, -(-N // 128), K // 128) * np.float32(2.0 ** -12)
+    off = np.array([0, 0, 2 * M, R], np.int32)
+    X, XS, W, WS, O = on(dev, x, xs, w, ws, off)
+    assert pkg.w8a8_kernel(R, E) == pkg.W8A8_KERNEL_SKINNY
+    want, mag = ref.grouped(x, xs, None, off, w, ws, R)
+    got = pkg.w8a8_gemm_grouped(X, XS, None, O, W, WS, dtype=TYPES[dtype])
+    close(got, want, ref.bound(mag, want, K, dtype, False), f"by expert {M} {N} {K}")
+    want, mag = ref.gemm(x[:M], xs[:M], w[0], ws[0])
+    got = pkg.w8a8_gemm(X[:M], XS[:M], W[0], WS[0], dtype=TYPES[dtype])
+    close(got, want, ref.bound(mag, want, K, dtype, False), f"{M} {N} {K}")
+    for block in (0, 15, K // 128 - 1):
+        bad = W[0].clone()
+        bad[N - 1, 128 * block + 77] = 0x7F
+        nan = pkg.w8a8_gemm(X[:M], XS[:M], bad, WS[0], dtype=TYPES[dtype]).isnan()
+        assert bool(nan[:, N - 1].all()) and int(nan.sum()) == M
+
+
 @pytest.mark.parametrize("E,R", [(65535, 100), (3000, 31000), (1025, 2000)])
 def test_many_experts(dev, E, R):
     rng = np.random.default_rng(E)
