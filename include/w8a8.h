@@ -111,7 +111,12 @@ int w8a8_rms_norm(const void *X, const void *residual, const void *weight, void 
  * in fp32.  With 16-bit outputs the kernel for many rows (W8A8_KERNEL_TILE) adds products
  * 8 at a time, cut off 13 bits below the largest one's power of two: at most 7 * 2^-13 of
  * sum |x w| off, in the root mean square 2^-16 of the result for normally distributed
- * values (2^-14 where a hundredth of them is 20 times the others).
+ * values (2^-14.5 where a hundredth of the activations is 20 times the others, 2^-14 where
+ * that holds for the weights as well).  That adds 0.2% to the error of stored fp16 results
+ * (1.2%, 4%; 6.5% with a twentieth of both operands 50 times the others), and at most 0.1% to
+ * bf16's.  fp32 outputs, and any of W8A8_KERNEL_SKINNY, have no such cut; who wants 16-bit
+ * results without it takes fp32 ones and rounds them.  So a row's result may differ by it,
+ * beside fp32 sums' order, between a call of few rows and one of many.
  * The scales' products xs * ws are formed in fp32 and have to stay in its normal range.
  * A NaN code or scale gives NaN in the outputs that it enters.
  * Which kernel runs: w8a8_kernel.  M == 0 or N == 0 is a no-op.  W4A16_ERR_ARG for

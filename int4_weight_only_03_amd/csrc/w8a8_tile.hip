@@ -4,10 +4,12 @@
 // rows of W, B: 16 slots, C: 0), and one fp32 FMA per output adds it up with its scales'
 // product.  The fp8 instructions add products 8 at a time, each cut off 13 bits below the
 // largest one's power of two (measured; the sums of 8 then add up in fp32), which moves a
-// result by at most 7 * 2^-13 of sum |x w| and, on normally distributed values, by 2^-16 in
-// the root mean square: little beside 16-bit outputs' own rounding, and half the time of
-// anything that is exact.  fp32 outputs take the codes as fp16, exactly, on the 16x16x32 fp16
-// instructions instead.
+// result by at most 7 * 2^-13 of sum |x w| and, on normally distributed values, by 2^-16.1 in
+// the root mean square (2^-14.9 where a hundredth of the activations is 20 times the others,
+// 2^-14.05 where the weights are so too).  Stored bf16 results are further off by 0.0% to 0.1%
+// for it, fp16 ones by 0.2%, 1.2% and 4% (6.5% with a twentieth of both 50 times the others), and
+// anything that is exact takes twice the time (4096 x 4096 x 7168: 101 us, 218).  fp32 outputs
+// take the codes as fp16, exactly, on the 16x16x32 fp16 instructions instead.
 //
 // A tile is 16 WU GU slots by 16 WT GT rows of W: GU x GT waves take 16 WU slots by 16 WT rows
 // each, in turn, so that a half-full tile's work is spread over them.  G such groups of
