@@ -69,8 +69,9 @@ int w8a8_quantize_weights(const float *W, uint8_t *codes, float *scales, int64_t
  *                        and scales from there on are left as they were.
  *   codes     uint8 [M][K], scales float [M][KB]
  * swiglu != 0: v = g / (1 + exp(-g)) * u in fp32, g the row's first K values and u the
- * others (what a gate/up product of 2K rows gives); an infinite g of the sign where
- * the definition is 0 times infinity gives NaN.
+ * others (what a gate/up product of 2K rows gives), within 4 units of 2^-23 and 2^-148 |u|;
+ * below g = -88.72, where exp(-g) passes fp32's range, v is 0; an infinite g of the sign
+ * where the definition is 0 times infinity gives NaN.
  * M == 0 is a no-op.  W4A16_ERR_ARG for a NULL pointer (num_rows may be), an unknown
  * dtype, negative extents, K == 0 or an output that overlaps an input or the other
  * output; W4A16_ERR_SHAPE for K % 16 != 0 or an extent past W8A8_MAX_*;
