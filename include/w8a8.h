@@ -156,8 +156,8 @@ int w8a8_gemm_grouped(const uint8_t *X, const float *xs, const int32_t *token_in
 
 /* The kernel (one of W8A8_KERNEL_*) of w8a8_gemm for R rows (E = 0), or of
  * w8a8_gemm_grouped for R slots over E experts: the skinny one for up to 4 rows, or 10 slots
- * per expert (of the fewer of R and E).  0 for extents that are refused or a no-op.  Host
- * only. */
+ * per expert (of the fewer of R and E).  With it a slot's result does not depend on the other
+ * slots of the call.  0 for extents that are refused or a no-op.  Host only. */
 int w8a8_kernel(int64_t R, int64_t E);
 
 #ifdef __cplusplus

@@ -168,8 +168,9 @@ hipError_t run_norm_with(const NormArgs &a, hipStream_t stream) {
 
 template <typename XT>
 hipError_t run_norm(const NormArgs &a, hipStream_t stream) {
-  // few rows: one vector a thread (us with 256 threads of 4 vectors, with 1024 of one; K =
-  // 7168, bf16: 1 row 4.9, 3.3; 256 6.5, 4.5; 512 8.6, 7.4; 1024 11.4, 11.5)
+  // few rows: one vector a thread (us with 256 threads of 4 vectors, with 1024 of one; bf16, K =
+  // 7168: 1 row 4.9, 3.2; 256 6.5, 4.5; 512 8.7, 7.5; 1024 11.4, 11.5; K = 2080, where three
+  // quarters of the 1024 have nothing: 1 row 3.5, 2.9; 256 4.0, 3.5; 512 4.35, 4.25)
   if (a.M <= 512 && a.K > 256 && a.K <= 8192)
     return a.K <= 2048 ? run_norm_with<XT, 256, 1>(a, stream)
                        : run_norm_with<XT, 1024, 1>(a, stream);

@@ -29,7 +29,7 @@ struct SkinnyArgs {
   const float *ws;
   void *Y;
   int rows_x, R, E, N, K, KB, NB, tiles_n;
-  int turn;  // blocks that a workgroup begins behind the one before it
+  int turn;  // blocks that a tile of W begins behind the one before it
   bool vec;  // rows of Y begin and end at 4 outputs
 };
 
@@ -70,10 +70,12 @@ __global__ void __launch_bounds__(64 * KW) gemm8_skinny(SkinnyArgs a) {
     float s, t;
   };
   // Rows of 4096 bytes, or a multiple, have their blocks in the same few channels of memory:
-  // there workgroups begin 2 KB behind each other and go round (64 slots of 32 experts of 4096 x
-  // 8192: 229 us, 179 so; of 4096 x 4096 98, 92; 1 row 6.1, 5.7); at other lengths, which need
-  // none of it, that costs up to 2%.
-  const int turn = a.turn ? int(blockIdx.x * unsigned(a.turn) % unsigned(a.KB)) : 0;
+  // there tiles begin 2 KB behind each other and go round (64 slots of 32 experts of 4096 x
+  // 8192: 229 us, 180 so; of 4096 x 4096 98, 92; 1 row 6.1, 5.7); other lengths need none of it
+  // and lose up to 3% (32 experts of 4096 x 2048 46.2, 46.6; of 4096 x 6144 133.8, 134.6; 1 row of
+  // the latter 6.6, 6.8).  By the tile of W alone: a slot's sums have the same order whatever
+  // other slots there are.
+  const int turn = a.turn ? int(unsigned(tile) * unsigned(a.turn) % unsigned(a.KB)) : 0;
   auto block_of = [&](int i) { return i + turn < a.KB ? i + turn : i + turn - a.KB; };
   auto load = [&](Step &s, int i) {
     const int b = block_of(i);
