@@ -85,8 +85,8 @@ int w8a8_quantize(const void *X, const int32_t *num_rows, uint8_t *codes, float 
  *     h = X + residual                      (fp32; residual may be NULL: h = X)
  *     y = h * weight / sqrt(mean(h^2) + eps)   (fp32)
  *     H = h, Y = y rounded to dtype; codes, scales = y as w8a8_quantize
- * y comes from h before H's rounding.  Sums of squares past fp32's range, or far
- * below its least, are formed from the row scaled by a power of two.  As the formula
+ * y comes from h before H's rounding.  Sums of squares past fp32's range (with eps), or
+ * far below its least, are formed from the row scaled by a power of two.  As the formula
  * has it, an infinity in h gives NaN there and 0 in the rest of its row, a NaN gives
  * NaN in all of it.
  *   X, residual  [M][K], dtype; weight [K], weight_dtype (dtype or W4A16_DTYPE_F32)

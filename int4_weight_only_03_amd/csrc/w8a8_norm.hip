@@ -103,10 +103,11 @@ rms_norm_rows(NormArgs a) {
     }
   }
   sum = row_sum<TPR>(sum, lds);
-  // 2^e scales the row where its squares leave fp32's range, or come so near its least
-  // (their sum, or eps) that bits of it are lost
+  // 2^e scales the row where its squares or their sum with eps leave fp32's range, or come so
+  // near its least (their sum, or eps) that bits of it are lost
   float factor;
-  if (!(sum < 0x1p127f) || (sum < 0x1p-60f && a.eps < 0x1p-60f)) {  // the same in all lanes
+  if (!(sum < 0x1p127f) || a.eps >= 0x1p126f ||
+      (sum < 0x1p-60f && a.eps < 0x1p-60f)) {  // the same in all lanes
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j)
