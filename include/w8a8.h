@@ -123,7 +123,8 @@ int w8a8_rms_norm(const void *X, const void *residual, const void *weight, void 
  * Which kernel runs: w8a8_kernel.  M == 0 or N == 0 is a no-op.  W4A16_ERR_ARG for
  * NULL pointers, negative extents, K == 0, block != 128, an unknown dtype or Y
  * overlapping an input; W4A16_ERR_SHAPE for K % 16 != 0, an extent past W8A8_MAX_*, or
- * tiles that would take 2^32 threads or more; W4A16_ERR_ALIGN for X or W not
+ * where tiles of every size would take 2^32 threads or more (W8A8_KERNEL_SKINNY has one size,
+ * 16 rows of W by 512 threads, by expert 32 by 256); W4A16_ERR_ALIGN for X or W not
  * 16-byte aligned, the scales not 4 and Y not to its elements.
  */
 int w8a8_gemm(const uint8_t *X, const float *xs, const uint8_t *W, const float *ws, void *Y,

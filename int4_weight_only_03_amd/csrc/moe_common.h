@@ -7,6 +7,7 @@
 
 #include <cstdint>
 
+#include "launch_limits.h"
 #include "w4a16_internal.h"
 
 namespace w4a16 {
@@ -43,9 +44,6 @@ __device__ __forceinline__ void expert_slots(const int32_t *__restrict__ offsets
   r0 = min(max(offsets[e], 0), R);
   r1 = min(max(offsets[e + 1], r0), R);
 }
-
-// A launch of 256 threads a workgroup has at most this many (2^32 threads).
-constexpr long kMaxBlocks = (1L << 24) - 8;
 
 struct ExpertItem {
   int e;      // expert, -1 behind the last item
@@ -118,13 +116,6 @@ __device__ __forceinline__ ExpertItem find_item(const int32_t *__restrict__ offs
   it.block = __builtin_amdgcn_readlane(block, owner);
   it.blocks = __builtin_amdgcn_readlane(blocks, owner);
   return it;
-}
-
-// The most items there can be: every expert with a slot adds at most one
-// partly filled block.
-inline long max_items(long R, long E, long B) {
-  const long active = R < E ? R : E;
-  return (R + (B - 1) * active) / B;
 }
 
 // Lane row R (16 lanes) holds words 0..3 of group R in v0..v3; afterwards word

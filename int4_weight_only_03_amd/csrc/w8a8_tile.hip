@@ -39,10 +39,10 @@
 // Tiles are dealt so that each XCD works a contiguous run of them (the hardware deals
 // workgroups round-robin over the 8 XCDs); see in_band for their order.
 
+#include "w8a8_choice.h"
 #include "w8a8_common.h"
 
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 namespace w4a16 {
@@ -488,6 +488,8 @@ gemm8_tile(TileArgs a) {
   }
 }
 
+TileCall call_of(const Gemm8 &p) { return {p.R, p.E, p.N, p.K, p.expert_offsets != nullptr}; }
+
 template <int WU, int WT, int GU, int GT, int G, int S, typename OT, bool kExact>
 hipError_t run_tile8(const Gemm8 &p, hipStream_t stream) {
   constexpr int TM = 16 * WU * GU, TN = 16 * WT * GT;
@@ -509,98 +511,17 @@ hipError_t run_tile8(const Gemm8 &p, hipStream_t stream) {
   a.tiles_n = int((long(p.N) + TN - 1) / TN);
   constexpr int kV = 16 / sizeof(OT);
   a.vec = p.N % kV == 0 && reinterpret_cast<uintptr_t>(p.Y) % 16 == 0;
-  const long items =
-      p.expert_offsets ? max_items(p.R, p.E, TM) : (long(p.R) + TM - 1) / TM;
-  const long tiles = items * a.tiles_n;
-  if (tiles > kMaxBlocks * 4 / (GU * GT * G) - 8) return hipErrorInvalidConfiguration;
+  const long tiles = tiles_of(TM, TN, call_of(p), p.R);
+  if (tiles > most_tiles(GU * GT * G)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((gemm8_tile<WU, WT, GU, GT, G, S, OT, kExact>),
                      dim3(unsigned((tiles + 7) / 8 * 8)), dim3(64 * GU * GT * G), 0, stream, a);
   return hipGetLastError();
 }
 
-// Tiles of `slots` x `rows`, and the time of a launch in which every compute unit has one
-// (us, 56 blocks of K) or `per_cu` of them, by measurement.
-struct Choice {
-  int slots, rows, per_cu;
-  double one, all;
-};
-constexpr Choice kChoices[] = {
-    {16, 32, 1, 7.7, 7.7},      // 4 groups of waves over K, 4 images
-    {32, 32, 1, 9.2, 9.2},      // the same
-    {32, 64, 1, 12.3, 12.3},    // 2 groups, 4 images
-    {64, 64, 1, 16.8, 16.8},    // the same
-    {64, 64, 2, 19.6, 30.0},    // 4 images
-    {64, 128, 1, 25.0, 25.0},   // 4 images
-    {128, 128, 1, 39.2, 39.2},  // 4 images
-    {128, 128, 2, 49.0, 66.0},  // 2 images
-    {256, 256, 1, 100.0, 100.0},
-};
-constexpr Choice kExactChoices[] = {  // fp32 outputs: no more registers for larger tiles
-    {16, 32, 1, 9.5, 9.5},    {32, 32, 1, 12.0, 12.0},  {32, 64, 1, 18.0, 18.0},
-    {64, 64, 1, 23.5, 23.5},  {64, 64, 2, 31.3, 40.0},  {128, 128, 2, 66.0, 110.0},
-};
-
-// Time of a choice: rounds of tiles over 256 compute units.  An expert's last tile is on the
-// average half empty, and one of 128 slots or more that is takes less time (32 experts of 4096
-// x 7168, bf16, us with 128 and 256 slots: mean 64 197, 206; 94 268, 217; 128 273, 239; 188
-// 343, 340; 256 404, 351).
-double time_of(const Choice &c, const Gemm8 &p, long R) {
-  const double experts = p.expert_offsets ? std::min(p.R, p.E) : 1;
-  const double items = p.expert_offsets ? experts * std::max(1.0, R / experts / c.slots + 0.5)
-                                        : double((R + c.slots - 1) / c.slots);
-  const double tiles = items * double((long(p.N) + c.rows - 1) / c.rows);
-  const double rounds = std::floor(tiles / (256 * c.per_cu));
-  const double rest = tiles - rounds * 256 * c.per_cu;
-  // A round that leaves half of the card idle is up to a fifth faster (256 x 256: 64 tiles 80,
-  // 128 82, 168 83, 256 103).
-  const double part = rest <= 256.0 ? c.one * (0.8 + 0.2 * std::max(0.0, rest / 128 - 1.0)) : c.all;
-  const double t = rounds * c.all + (rest > 0.0 ? part : 0.0);
-  return p.expert_offsets && c.slots >= 128
-             ? t * (0.5 + 0.5 * std::min(1.0, R / experts / c.slots))
-             : t;
-}
-
-struct Best {
-  int choice;
-  double time;
-};
-template <int kCount>
-Best least(const Choice (&list)[kCount], const Gemm8 &p, long R) {
-  Best best = {0, time_of(list[0], p, R)};
-  for (int i = 1; i < kCount; ++i) {
-    const double t = time_of(list[i], p, R);
-    if (t < best.time) best = {i, t};
-  }
-  return best;
-}
-
-// Rows of X that one launch takes, whole rounds of its tiles, before another takes the rest
-// (all of them: one launch is the best).  Only where a round is worth it beside a launch (2
-// us) and the host's own time.  us with one launch and with two, bf16: 1030 x 4096 x 7168 56,
-// 44; 4100 165, 106; fp32 101, 80.
-template <int kCount>
-long rows_before_rest(const Choice (&list)[kCount], const Gemm8 &p) {
-  const double blocks = blocks8(p.K) / 56.0;
-  double least_time = least(list, p, p.R).time;
-  long rows = p.R;
-  if (p.expert_offsets || least_time * blocks < 25.0) return rows;
-  for (const Choice &c : list) {
-    const long tiles_n = (long(p.N) + c.rows - 1) / c.rows, round = 256L * c.per_cu;
-    const long tiles = (long(p.R) + c.slots - 1) / c.slots * tiles_n;
-    const long first = tiles / round * round / tiles_n * c.slots;
-    if (first <= 0 || first >= p.R) continue;
-    const double t = least(list, p, first).time + least(list, p, p.R - first).time + 2.0 / blocks;
-    if (t < least_time) {
-      least_time = t;
-      rows = first;
-    }
-  }
-  return rows;
-}
-
 template <typename OT>
 hipError_t run_type8(const Gemm8 &p, hipStream_t stream) {
-  switch (least(kChoices, p, p.R).choice) {
+  switch (least(kChoices, call_of(p), p.R).choice) {
+    case -1: return hipErrorInvalidConfiguration;
     case 0: return run_tile8<1, 1, 1, 2, 4, 4, OT, false>(p, stream);
     case 1: return run_tile8<1, 1, 2, 2, 4, 4, OT, false>(p, stream);
     case 2: return run_tile8<1, 2, 2, 2, 2, 4, OT, false>(p, stream);
@@ -614,7 +535,8 @@ hipError_t run_type8(const Gemm8 &p, hipStream_t stream) {
 }
 
 hipError_t run_exact8(const Gemm8 &p, hipStream_t stream) {
-  switch (least(kExactChoices, p, p.R).choice) {
+  switch (least(kExactChoices, call_of(p), p.R).choice) {
+    case -1: return hipErrorInvalidConfiguration;
     case 0: return run_tile8<1, 1, 1, 2, 4, 4, float, true>(p, stream);
     case 1: return run_tile8<1, 1, 2, 2, 4, 4, float, true>(p, stream);
     case 2: return run_tile8<1, 2, 2, 2, 2, 4, float, true>(p, stream);
@@ -649,7 +571,8 @@ hipError_t launch_gemm8_tile(const Gemm8 &p, hipStream_t stream) {
     }
   };
   const bool exact = p.dtype == W4A16_DTYPE_F32;
-  const long rows = exact ? rows_before_rest(kExactChoices, p) : rows_before_rest(kChoices, p);
+  const long rows = exact ? rows_before_rest(kExactChoices, call_of(p))
+                          : rows_before_rest(kChoices, call_of(p));
   Gemm8 part = p;
   part.R = part.rows_x = int(rows);
   if (p.expert_offsets) part.rows_x = p.rows_x;
