@@ -83,7 +83,7 @@ Best least(const Choice (&list)[kCount], const TileCall &p, long R) {
 // Rows of X that one launch takes, whole rounds of its tiles, before another takes the rest
 // (all of them: one launch is the best).  Only where a round is worth it beside a launch (2
 // us) and the host's own time.  us with one launch and with two, bf16: 1030 x 4096 x 7168 56,
-// 44; 4100 165, 106; fp32 101, 80.
+// 43; 4100 165, 106; fp32 101, 80.
 template <int kCount>
 long rows_before_rest(const Choice (&list)[kCount], const TileCall &p) {
   const double blocks = double((p.K + 127) / 128) / 56.0;

@@ -67,9 +67,9 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m) {
 // Codes of a group's values, 8 to a lane, and the group's scale.  Every one of the
 // group's 16 lanes has to call it (those behind the row's end with zeros).
 // Magnitudes are compared as integers, so that a NaN is the largest of all.
-// v / scale: v times the reciprocal, mended by its remainder (v * f alone is 2^-22 off at
-// most and, near a tie of e4m3, on the other side of it four times as often as the
-// quotient rounded to fp32).  The largest value's is at most 448 (1 + 2^-23), which rounds
+// v / scale: v times the reciprocal, mended by its remainder, which is the quotient rounded to
+// fp32 but once in 10^8 (v * f alone is 2^-22 off at most and, near a tie of e4m3, on the
+// other side of it four times as often).  The largest value's is at most 448 (1 + 2^-23), which rounds
 // to 448.
 __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float &scale) {
   uint32_t m = 0;

@@ -22,9 +22,9 @@
 //
 // Few tiles are bound by latency: a stage takes 0.4 us whatever is in it (64 x 64, one group,
 // 256 x 4096 x 7168: 19.6 us), so groups and small tiles, which put more of K and more of the
-// card to work, win until the tiles are more than the card (64 x 64 with two groups 17.1; 64
-// rows with 32 x 32 and four 10.4).  The largest are bound by power: 256 x 256 runs 8192 x 8192
-// x 8192 in 464 us, 2.37 PFLOP/s, the matrix units busy for 56% of the cycles at 1.9 GHz (2.4
+// card to work, win until the tiles are more than the card (64 x 64 with two groups 16.9; 64
+// rows with 32 x 32 and four 10.5).  The largest are bound by power: 256 x 256 runs 8192 x 8192
+// x 8192 in 455 us, 2.4 PFLOP/s, the matrix units busy for 56% of the cycles at 1.9 GHz (2.4
 // without load); left out, the copies between L2 and LDS would save 18%, the FMAs 5%, operand
 // reads from LDS nothing.  Instructions and FMAs alone, in registers, reach 3.7 PFLOP/s.
 // Tried without gain there: operands 1 to 3 steps ahead, copies at once or spread over the
@@ -421,7 +421,7 @@ gemm8_tile(TileArgs a) {
   const int n = 16 * WT * wt + 4 * WT * R, cols = std::min(TN, a.N - n0);  // of the tile
   // Whole vectors straight from the sums, where they are a good part of a cache line: of fp32
   // in tiles of 128 rows a lane's 16 outputs take four stores, each to 64 places, and the way
-  // through LDS below is the faster (4096 x 4096 x 1024: 51.6 us, 45.7 so; 64 x 64 tiles and
+  // through LDS below is the faster (4096 x 4096 x 1024: 51.6 us, 44.3 so; 64 x 64 tiles and
   // 16-bit outputs lose by it: 500 x 1408 x 2064 11.9, 12.3; 4096 x 4096 x 1024 in bf16 22.5,
   // 26.2).
   if (a.vec && (sizeof(OT) == 2 || WT < 4)) {
@@ -445,8 +445,8 @@ gemm8_tile(TileArgs a) {
     return;
   }
   // Rows that begin anywhere: to LDS first, each row as far behind a multiple of 16 bytes as
-  // in memory, so that whole 16 bytes of it are read and stored (4096 x 4095 x 7168, bf16: 144
-  // us with single outputs stored from the sums).
+  // in memory, so that whole 16 bytes of it are read and stored (4096 x 4095 x 7168, bf16: 107
+  // us, 144 with single outputs stored from the sums).
   constexpr int kV = 16 / sizeof(OT), kPitch = TN + kV, kChunks = TN / kV + 1;
   constexpr int kPart = WU * 16 * GU * kPitch * sizeof(OT) <= sizeof(mem) ? WU : WU / 2;
   static_assert(kPart * 16 * GU * kPitch * sizeof(OT) <= sizeof(mem), "room for the outputs");
@@ -549,8 +549,11 @@ hipError_t run_exact8(const Gemm8 &p, hipStream_t stream) {
 }  // namespace
 
 // Few rows: the skinny kernel.  Of one expert (4096 rows of W x 7168, us skinny against the
-// tiles): 1 row 7.1, 7.4 (fp32 outputs 9.3), 16 rows 10.5, 8.1; of many by their mean (32 of
-// the same): 2 156, 168; 8 167, 182; 16 240, 176.
+// tiles): 1 row 7.1, 7.7 (fp32 outputs 7.2, 9.3), 4 rows 7.8, 7.8, 16 rows 10.4, 8.1; of many by
+// their mean (32 of the same): 2 155, 159; 8 167, 160 (fp32 168, 170); 10 175, 160 (176, 171); 16
+// 246, 162 (247, 177); 60 of 2080 x 1408 with 4 36.1, 36.9 (36.5, 41.3), with 10 39.4, 37.4
+// (39.8, 44.3).  Up to 10 they are within a tenth of each other, either way, and the skinny
+// kernel's sums are exact.
 int gemm8_kernel(long R, long E, bool grouped) {
   if (!grouped) return R <= 4 ? W8A8_KERNEL_SKINNY : W8A8_KERNEL_TILE;
   return R <= 10 * std::max(1L, std::min(R, E)) ? W8A8_KERNEL_SKINNY : W8A8_KERNEL_TILE;
